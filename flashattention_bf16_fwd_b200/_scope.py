@@ -1,0 +1,49 @@
+"""Device, stream and argument checks that the bindings of the window and cache calls share."""
+from __future__ import annotations
+
+import contextlib
+
+import torch
+
+_HERE = contextlib.nullcontext()
+
+
+def scope(t, stream):
+    """The context in which a call on tensor ``t`` allocates and launches: t's
+    device is current, and ``stream`` (a torch stream or a cudaStream_t; None:
+    the device's current stream) is the current stream, so that what the call
+    allocates belongs to the stream that uses it."""
+    if not t.is_cuda:
+        raise ValueError("tensors must live on a CUDA device (the library has no CPU path)")
+    if stream is None:
+        return _HERE if t.get_device() == torch.cuda.current_device() else torch.cuda.device(t.device)
+    if not isinstance(stream, torch.cuda.Stream):
+        stream = (torch.cuda.ExternalStream(int(stream), device=t.device) if int(stream)
+                  else torch.cuda.default_stream(t.device))
+    if stream.device != t.device:
+        raise ValueError(f"the stream is on {stream.device}, the tensors on {t.device}")
+    return torch.cuda.stream(stream)
+
+
+def current() -> int:
+    """The current device's current stream."""
+    return torch.cuda.current_stream().cuda_stream
+
+
+def same_device(t, *others):
+    for x in others:
+        if x is not None and x.device != t.device:
+            raise ValueError("tensors must share one device")
+
+
+def int32(name, t, shape):
+    """t: a contiguous int32 tensor of this shape (None: any length)."""
+    if t.dtype != torch.int32 or t.dim() != len(shape) or not t.is_contiguous() or any(
+            want is not None and have != want for have, want in zip(t.shape, shape)):
+        raise ValueError(f"{name} must be a contiguous int32 tensor of shape "
+                         f"[{', '.join('*' if n is None else str(n) for n in shape)}], got {t.dtype} {tuple(t.shape)}")
+
+
+def count(n) -> int:
+    """n as a C int: more than an int holds is as much as the largest one."""
+    return max(-1, min(int(n), 2**31 - 1))

@@ -12,15 +12,16 @@ import sys
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
 LIB = os.path.join(PKG, "libfa_b200.so")
-SOURCES = [os.path.join(PKG, "csrc", "fa_api.cu")]
-HEADERS = [os.path.join(PKG, "csrc", f) for f in ("sm100.cuh", "fa_fwd.cuh", "fa_bwd.cuh")] + [
-    os.path.join(ROOT, "include", "fa_b200.h")]
+SOURCES = [os.path.join(PKG, "csrc", f) for f in ("fa_api.cu", "fa_cache.cu")]
+HEADERS = [os.path.join(PKG, "csrc", f) for f in ("sm100.cuh", "fa_fwd.cuh", "fa_bwd.cuh", "fa_selftest.cuh",
+                                                  "fa_host.h", "fa_cache.cuh", "fa_decode.cuh")] + [
+    os.path.join(ROOT, "include", f) for f in ("fa_b200.h", "fa_b200_cache.h")]
 
 NVCC_FLAGS = [
     "-gencode", "arch=compute_100a,code=sm_100a",
     "-O3", "-lineinfo", "-std=c++17", "--use_fast_math",
     "-shared", "-Xcompiler", "-fPIC", "-Xcompiler", "-fvisibility=hidden",
-    "-cudart", "static",
+    "-cudart", "static", "--threads", "0",
 ]
 
 

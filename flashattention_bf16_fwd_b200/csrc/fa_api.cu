@@ -10,8 +10,10 @@
 #include <utility>
 
 #include "../../include/fa_b200.h"
+#include "../../include/fa_b200_cache.h"
 #include "fa_bwd.cuh"
 #include "fa_fwd.cuh"
+#include "fa_host.h"
 #include "fa_selftest.cuh"
 
 namespace fa {
@@ -35,6 +37,8 @@ DeviceState g_devices[kMaxDevices];
 PFN_cuTensorMapEncodeTiled_v12000 g_encode = nullptr;
 std::once_flag g_encode_once;
 
+}  // namespace
+
 PFN_cuTensorMapEncodeTiled_v12000 encoder() {
   std::call_once(g_encode_once, [] {
     void* fn = nullptr;
@@ -45,6 +49,8 @@ PFN_cuTensorMapEncodeTiled_v12000 encoder() {
   });
   return g_encode;
 }
+
+namespace {
 
 // Per-device set-up, done once with that device current: check the
 // architecture, opt the kernels into large shared memory, and resolve the
@@ -102,30 +108,6 @@ DeviceState* device_state(int* why = nullptr) {
   int var##_why = FA_ERR_DEVICE;              \
   DeviceState* var = device_state(&var##_why); \
   if (!var) return var##_why
-
-bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
-
-// Every kernel is launched with programmatic stream serialisation: it may be
-// scheduled while the previous kernel in the stream drains, runs its set-up
-// (barriers, TMEM, descriptor prefetch), and waits in grid_dep_wait() before
-// it touches global memory.
-constexpr int kProgrammaticLaunch = 1;
-
-template <typename... KArgs, typename... Args>
-cudaError_t launch(void (*kernel)(KArgs...), dim3 grid, dim3 block, size_t smem, cudaStream_t stream,
-                   Args&&... args) {
-  cudaLaunchConfig_t cfg{};
-  cfg.gridDim = grid;
-  cfg.blockDim = block;
-  cfg.dynamicSmemBytes = smem;
-  cfg.stream = stream;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = kProgrammaticLaunch;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, kernel, std::forward<Args>(args)...);
-}
 
 int check_common(int B, int H, int N, int d, int causal, float scale) {
   if (d != 64 && d != 128) return FA_ERR_HEADDIM;
@@ -239,6 +221,14 @@ int launch_fwd(const void* q, const void* k, const void* v, void* o, float* lse,
 size_t align256(size_t x) { return (x + 255) & ~size_t(255); }
 
 }  // namespace
+
+int host_device(int* num_sms, int** dev_error) {
+  FA_DEVICE_OR_RETURN(st);
+  *num_sms = st->num_sms;
+  *dev_error = st->dev_error;
+  return FA_OK;
+}
+
 }  // namespace fa
 
 using namespace fa;
@@ -473,6 +463,11 @@ const char* fa_status_string(int status) {
              "does not expect (rebuild with the flags in build.py)";
     case FA_ERR_SCRATCH_LIMIT:
       return "fa_bwd_noalloc: fa_bwd_workspace_size() exceeds FA_BWD_NOALLOC_SCRATCH_BYTES (32 MiB)";
+    case FA_ERR_PAGES:
+      return "a kernel found a page number, length or sequence index of the cache out of range (device error flag set)";
+    case FA_ERR_CACHE_SHAPE:
+      return "a cache argument is out of range: the page size, the number of pages, sequences or tokens, a row "
+             "stride, or the window";
     default: return "unknown status";
   }
 }
@@ -493,7 +488,7 @@ int fa_check_device_error(void* stream) {
   if (flag != kDevErrNone) {
     const int zero = 0;
     cudaMemcpy(st->dev_error, &zero, sizeof(int), cudaMemcpyHostToDevice);
-    return flag == kDevErrTimeout ? FA_ERR_TIMEOUT : FA_ERR_DEVICE;
+    return flag == kDevErrTimeout ? FA_ERR_TIMEOUT : flag == kDevErrPages ? FA_ERR_PAGES : FA_ERR_DEVICE;
   }
   return FA_OK;
 }

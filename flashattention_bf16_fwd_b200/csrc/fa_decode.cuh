@@ -1,0 +1,595 @@
+// fa_decode.cuh - attention of one new token per sequence over a paged cache.
+//
+// Per sequence and query head, over the keys j that it sees:
+//   x_j = scale q.K_j,  O = sum_j e^(x_j - m) V_j / sum_j e^(x_j - m),
+//   LSE = m + log sum_j e^(x_j - m).
+// Every K and V element is used by the group of query heads that share it and
+// by nothing else, so the bound is the bandwidth at which the visible tokens
+// come out of HBM; the arithmetic only has to stay out of the way.
+//
+// Work.  The keys of a sequence are cut into tiles of 64; the tiles of all
+// (sequence, key/value head) units, laid end to end, are divided evenly among
+// the CTAs, whatever the lengths: each CTA takes one stretch.  A unit that lies
+// in one stretch is finished there; one that is cut leaves unnormalised
+// partial results (O, m, l), at most two per CTA, which fa_decode_join_kernel
+// puts together.  The cut depends on lens alone, so that sums always run in
+// the same order.
+//
+// A CTA: warp 4 fetches tiles with TMA, one box per page piece (or per 64 keys)
+// and 64 elements of d, into a ring; warps 0-3 take 16 keys of a tile each and
+// keep a running maximum, sum and O of their own in registers, so that they
+// meet only at the end of a unit.
+// The products run on mma.sync with the keys as rows, S^T = K Q^T and
+// O^T = V^T P^T: 8 query heads are one N = 8 tile, where tcgen05 would spend
+// 128 rows on them.  P enters as P_hi + P_lo, two values of the element format:
+// two products instead of one, on a tensor core that is idle otherwise, and no
+// rounding of P in O.
+#pragma once
+
+#include "sm100.cuh"
+
+namespace fa {
+
+struct DecodeParams {
+  const void* q;         // [S, H, D], q_stride elements between sequences
+  const int32_t* table;  // [S, M]
+  const int32_t* lens;   // [S]
+  void* o;               // [S, H, D]
+  float* lse;            // [S, H]
+  int32_t* cum;          // workspace: [S + 1] tiles before each sequence
+  float* part;           // workspace: [2 * CTAs] partial results
+  int* dev_error;
+  long long q_stride;
+  int S, H, group, units;   // query heads per K/V head; units per sequence (K/V heads x head blocks)
+  int blocks;               // head blocks per K/V head
+  int P, page, M, box;      // box: keys per TMA box (a divisor of 64 and of page)
+  int z_none;               // a third TMA coordinate past the cache: the box reads as zeros
+  int window, sinks;
+  int ctas;                 // CTAs that the tiles are divided among
+  float scale_log2;
+};
+
+constexpr int kDecTile = 64;       // keys per tile
+constexpr int kDecMaxSeqs = 8192;
+constexpr int kDecMaxCtas = 320;   // two per SM
+
+template <int D, int NB>
+struct DecLayout {
+  static constexpr int kSub = D / 64;
+  static constexpr int kSubBytes = kDecTile * 128;           // 64 keys x 64 elements
+  static constexpr int kTileBytes = kSub * kSubBytes;
+  static constexpr int kStages = (D == 64) ? 6 : 3;          // 96 KB of K and V in flight per CTA, two CTAs per SM
+  static constexpr int kJoinOff = kStages * 2 * kTileBytes;  // [4 warps][8 NB heads][kJoinRow] floats
+  static constexpr int kJoinCols = 64 / NB;                  // columns of d joined at a time
+  static constexpr int kJoinRow = kJoinCols + 4;             // rows 4 banks apart: the warps' writes do not collide
+  static constexpr int kMlOff = kJoinOff + 4 * 8 * NB * kJoinRow * 4;    // [4 warps][8 NB] m and l
+  static constexpr int kBarOff = kMlOff + 4 * 8 * NB * 2 * 4;
+  static constexpr int kCumOff = kBarOff + 256;              // [S + 1] int32
+  static constexpr int kThreads = 160;
+  static size_t bytes(int S) { return size_t(kCumOff) + (size_t(S) + 1) * 4 + 1024; }
+};
+
+// The tiles of a sequence: those with a sink, then those of the window (all
+// keys where nothing is hidden).
+struct DecSpan {
+  int n, lo, sk;    // visible: key < n and (key >= lo or key < sk)
+  int st, skip;     // tiles before the gap; tiles in the gap
+  int nt;           // tiles
+};
+
+__device__ __forceinline__ DecSpan dec_span(const DecodeParams& p, int len) {
+  DecSpan s;
+  s.n = min(max(len, 0), p.M * p.page);
+  s.lo = p.window > 0 ? max(0, s.n - p.window) : 0;
+  s.sk = min(p.sinks, s.n);
+  const int all = (s.n + kDecTile - 1) / kDecTile;
+  s.st = min((s.sk + kDecTile - 1) / kDecTile, all);
+  s.skip = max(0, s.lo / kDecTile - s.st);
+  s.nt = all - s.skip;
+  return s;
+}
+
+__device__ __forceinline__ int dec_key0(const DecSpan& s, int t) {
+  return (t < s.st ? t : t + s.skip) * kDecTile;
+}
+
+// First tile of CTA c's stretch when T tiles are divided among G CTAs.
+__device__ __forceinline__ long long dec_cut(long long T, int G, int c) { return T * c / G; }
+
+// A walk over one CTA's stretch of tiles.
+struct DecWalk {
+  int s, unit, t;
+  __device__ __forceinline__ void start(const int32_t* cum, int S, int units, long long x) {
+    int a = 0, b = S;               // the last s with cum[s] * units <= x and tiles of its own
+    while (b - a > 1) {
+      const int mid = (a + b) >> 1;
+      if ((long long)cum[mid] * units <= x) a = mid; else b = mid;
+    }
+    s = a;
+    const int nt = cum[s + 1] - cum[s];
+    const int r = int(x - (long long)cum[s] * units);
+    unit = nt > 0 ? r / nt : 0;
+    t = nt > 0 ? r % nt : 0;
+  }
+  __device__ __forceinline__ void next(const int32_t* cum, int S, int units) {
+    if (++t < cum[s + 1] - cum[s]) return;
+    t = 0;
+    if (++unit < units) return;
+    unit = 0;
+    do ++s; while (s < S && cum[s + 1] == cum[s]);
+  }
+};
+
+__device__ __forceinline__ void ldsm4(uint32_t (&r)[4], uint32_t addr) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(addr));
+}
+__device__ __forceinline__ void ldsm4_t(uint32_t (&r)[4], uint32_t addr) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(addr));
+}
+// The transpose of an 8 x 8 matrix of 16-bit elements held across the warp.
+__device__ __forceinline__ uint32_t transpose8(uint32_t x) {
+  uint32_t y;
+  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+  return y;
+}
+template <typename E>
+__device__ __forceinline__ void mma16816(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+  if constexpr (E::kMmaFmt == 1)
+    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+                 : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+                 : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+  else
+    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+                 : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+                 : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+
+// NB: blocks of 8 query heads that one CTA takes together.
+template <int D, int NB, typename E>
+__global__ void __launch_bounds__(160, 2)
+    fa_decode_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
+                     const DecodeParams p) {
+  using L = DecLayout<D, NB>;
+  using T = typename E::T;
+  constexpr float kLn2 = 0.69314718055994531f;
+  const float kNegInf = -__int_as_float(0x7f800000);
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  float* join = reinterpret_cast<float*>(smem + L::kJoinOff);
+  float* ml = reinterpret_cast<float*>(smem + L::kMlOff);
+  uint64_t* full = reinterpret_cast<uint64_t*>(smem + L::kBarOff);
+  uint64_t* empty = full + L::kStages;
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(empty + L::kStages);
+  int* warp_sum = reinterpret_cast<int*>(smem + L::kBarOff + 128);
+  int32_t* cum = reinterpret_cast<int32_t*>(smem + L::kCumOff);
+  const int warp = int(warp_id()), lane = int(lane_id());
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < L::kStages; ++s) {
+      mbar_init(&full[s], 1);
+      mbar_init(&empty[s], 4);
+    }
+    *abort_flag = 0;
+    fence_mbar_init();
+    tma_prefetch_desc(&tm_k);
+    tma_prefetch_desc(&tm_v);
+  }
+  grid_dep_wait();
+  grid_dep_launch();
+
+  // cum: tiles before each sequence.  Each thread sums a run of sequences, the
+  // runs are scanned over the CTA.
+  const int run = (p.S + L::kThreads - 1) / L::kThreads;
+  const int s_begin = min(p.S, int(threadIdx.x) * run), s_end = min(p.S, s_begin + run);
+  int mine = 0;
+  bool bad = false;
+  for (int s = s_begin; s < s_end; ++s) {
+    const int len = p.lens[s];
+    bad |= len < 0 || len > p.M * p.page;
+    mine += dec_span(p, len).nt;
+    cum[s + 1] = mine;
+  }
+  int before = mine;
+#pragma unroll
+  for (int d = 1; d < 32; d <<= 1) {
+    const int up = __shfl_up_sync(0xffffffffu, before, d);
+    if (lane >= d) before += up;
+  }
+  if (lane == 31) warp_sum[warp] = before;
+  before -= mine;
+  __syncthreads();
+  for (int w = 0; w < warp; ++w) before += warp_sum[w];
+  for (int s = s_begin; s < s_end; ++s) cum[s + 1] += before;
+  if (threadIdx.x == 0) cum[0] = 0;
+  if (bad && blockIdx.x == 0) atomicExch(p.dev_error, kDevErrPages);
+  __syncthreads();
+  if (blockIdx.x == 0)
+    for (int s = threadIdx.x; s <= p.S; s += L::kThreads) p.cum[s] = cum[s];
+  // empty sequences: O = 0, LSE = -inf
+  for (int s = blockIdx.x; s < p.S; s += gridDim.x) {
+    if (cum[s + 1] != cum[s]) continue;
+    for (int i = threadIdx.x; i < p.H * D / 8; i += L::kThreads)
+      reinterpret_cast<uint4*>(static_cast<T*>(p.o) + size_t(s) * p.H * D)[i] = make_uint4(0, 0, 0, 0);
+    for (int h = threadIdx.x; h < p.H; h += L::kThreads) p.lse[size_t(s) * p.H + h] = kNegInf;
+  }
+
+  const long long total = (long long)cum[p.S] * p.units;
+  const long long x0 = dec_cut(total, p.ctas, blockIdx.x), x1 = dec_cut(total, p.ctas, blockIdx.x + 1);
+  const int n_tiles = int(x1 - x0);
+  if (n_tiles == 0) return;
+  const Watchdog wd{abort_flag, p.dev_error};
+  DecWalk w;
+  w.start(cum, p.S, p.units, x0);
+
+  if (warp == 4) {
+    // ---------------------------------------------------------------- producer
+    // Lane b fetches box b of a tile (K and V).  The page number of the next
+    // tile's box is read before this tile's buffer is waited for.
+    const int boxes = kDecTile / p.box;
+    const uint64_t pol = l2_policy_evict_first();
+    const int hkv = p.units / p.blocks;
+    auto third = [&](const DecWalk& u) {       // the third TMA coordinate of this lane's box
+      if (lane >= boxes) return 0;
+      const DecSpan sp = dec_span(p, p.lens[u.s]);
+      const int key = dec_key0(sp, u.t) + lane * p.box;
+      const bool seen = key < sp.n && (key + p.box > sp.lo || key < sp.sk);
+      if (!seen) return p.z_none;
+      const int id = p.table[size_t(u.s) * p.M + key / p.page];
+      if (id < 0 || id >= p.P) {
+        atomicExch(p.dev_error, kDevErrPages);
+        return p.z_none;
+      }
+      return id * hkv + u.unit / p.blocks;
+    };
+    auto second = [&](const DecWalk& u) {
+      const DecSpan sp = dec_span(p, p.lens[u.s]);
+      return (dec_key0(sp, u.t) + lane * p.box) % p.page;
+    };
+    int z = third(w), row = second(w);
+    bool ok = true;
+    int i = 0;
+    for (; i < n_tiles; ++i) {
+      const int st = i % L::kStages;
+      ok = __all_sync(0xffffffffu, mbar_wait(&empty[st], ((i / L::kStages) & 1) ^ 1, wd));
+      if (!ok) break;
+      if (lane == 0) mbar_arrive_expect_tx(&full[st], uint32_t(2 * L::kTileBytes));
+      __syncwarp();
+      if (lane < boxes) {
+        uint8_t* sk = smem + st * 2 * L::kTileBytes + lane * p.box * 128;
+#pragma unroll
+        for (int s = 0; s < L::kSub; ++s) {
+          tma_load_3d(sk + s * L::kSubBytes, &tm_k, &full[st], s * 64, row, z, pol);
+          tma_load_3d(sk + L::kTileBytes + s * L::kSubBytes, &tm_v, &full[st], s * 64, row, z, pol);
+        }
+      }
+      if (i + 1 < n_tiles) {
+        w.next(cum, p.S, p.units);
+        z = third(w);
+        row = second(w);
+      }
+    }
+    // given up: the copies in flight still write this CTA's shared memory; wait
+    // for them (at most a second each) before the CTA ends
+    if (!ok) {
+      for (int k = max(0, i - L::kStages); k < i; ++k) {
+        const uint64_t end = globaltimer_ns() + 1000000000ull;
+        while (!mbar_try_wait(&full[k % L::kStages], (k / L::kStages) & 1) && globaltimer_ns() < end) {
+        }
+      }
+    }
+    return;
+  }
+
+  // ------------------------------------------------------------------ consumers
+  const int g = lane >> 2, tq = lane & 3;
+  uint32_t qf[D / 16][NB][2];
+  float ms[NB][2], l[NB][2], o[D / 16][NB][4];
+  bool ok = true, fresh = true;
+  bool first = true;                  // the stretch's first segment: partial slot 0
+  int seg_t0 = 0;
+  DecSpan sp{};
+  const uint32_t tile0 = smem_u32(smem);
+  const int row_k = warp * 16 + (lane & 15);                          // K: rows of the four matrices
+  const int row_v = warp * 16 + (lane & 7) + ((lane >> 4) << 3);      // V: keys of the four matrices
+
+  for (int i = 0; i < n_tiles; ++i) {
+    const int kvh = w.unit / p.blocks, h0 = kvh * p.group + (w.unit % p.blocks) * 8 * NB;
+    const int nh = min(8 * NB, (kvh + 1) * p.group - h0);
+    if (fresh) {
+      sp = dec_span(p, p.lens[w.s]);
+      seg_t0 = w.t;
+      const T* q = static_cast<const T*>(p.q) + size_t(w.s) * p.q_stride + size_t(h0) * D;
+#pragma unroll
+      for (int nb = 0; nb < NB; ++nb) {
+        const bool in = nb * 8 + g < nh;
+        const T* qr = q + (in ? nb * 8 + g : 0) * D + tq * 2;
+#pragma unroll
+        for (int k = 0; k < D / 16; ++k) {
+          qf[k][nb][0] = in ? *reinterpret_cast<const uint32_t*>(qr + k * 16) : 0u;
+          qf[k][nb][1] = in ? *reinterpret_cast<const uint32_t*>(qr + k * 16 + 8) : 0u;
+        }
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          ms[nb][e] = kNegInf;
+          l[nb][e] = 0.f;
+        }
+#pragma unroll
+        for (int k = 0; k < D / 16; ++k)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) o[k][nb][e] = 0.f;
+      }
+      fresh = false;
+    }
+    const int st = i % L::kStages;
+    if (ok) ok = __all_sync(0xffffffffu, mbar_wait(&full[st], (i / L::kStages) & 1, wd));
+    const int key0 = dec_key0(sp, w.t);
+    const int ka = key0 + warp * 16 + g, kb = ka + 8;     // this thread's rows of S^T
+    auto seen = [&](int key) { return key < sp.n && (key >= sp.lo || key < sp.sk); };
+    const int kw = key0 + warp * 16;
+    const bool whole = kw + 16 <= sp.n && (kw >= sp.lo || kw + 16 <= sp.sk);
+    const bool none = kw >= sp.n || (kw >= sp.sk && kw + 16 <= sp.lo);
+    if (ok && !none) {
+      const uint32_t tk = tile0 + st * 2 * L::kTileBytes, tv = tk + L::kTileBytes;
+      float c[NB][4];
+#pragma unroll
+      for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) c[nb][e] = 0.f;
+#pragma unroll
+      for (int k = 0; k < D / 16; ++k) {
+        uint32_t a[4];
+        ldsm4(a, tk + (k >> 2) * L::kSubBytes + row_k * 128 + ((((k & 3) * 2 + (lane >> 4)) ^ (row_k & 7)) << 4));
+#pragma unroll
+        for (int nb = 0; nb < NB; ++nb) mma16816<E>(c[nb], a, qf[k][nb][0], qf[k][nb][1]);
+      }
+      if (!whole) {
+        const bool sa = seen(ka), sb = seen(kb);
+#pragma unroll
+        for (int nb = 0; nb < NB; ++nb) {
+          c[nb][0] = sa ? c[nb][0] : kNegInf;
+          c[nb][1] = sa ? c[nb][1] : kNegInf;
+          c[nb][2] = sb ? c[nb][2] : kNegInf;
+          c[nb][3] = sb ? c[nb][3] : kNegInf;
+        }
+      }
+      uint32_t ph[NB][2], pl[NB][2];
+      bool moved = false;
+      float alpha[NB][2];
+#pragma unroll
+      for (int nb = 0; nb < NB; ++nb) {
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          float mx = fmaxf(c[nb][e], c[nb][e + 2]);
+          mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 4));
+          mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 8));
+          mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 16));
+          const float m_new = fmaxf(ms[nb][e], mx * p.scale_log2);
+          const float shift = m_new == kNegInf ? 0.f : m_new;
+          alpha[nb][e] = ex2(ms[nb][e] - shift);           // 0 where nothing was seen before
+          moved |= m_new != ms[nb][e];
+          ms[nb][e] = m_new;
+          c[nb][e] = ex2(fmaf(c[nb][e], p.scale_log2, -shift));
+          c[nb][e + 2] = ex2(fmaf(c[nb][e + 2], p.scale_log2, -shift));
+          l[nb][e] = fmaf(l[nb][e], alpha[nb][e], c[nb][e] + c[nb][e + 2]);
+        }
+#pragma unroll
+        for (int hv = 0; hv < 2; ++hv) {                    // keys 0-7, 8-15 of the warp's 16
+          const float a = c[nb][2 * hv], b = c[nb][2 * hv + 1];
+          const uint32_t hi = E::pack(a, b);
+          const float2 r = E::unpack(hi);
+          ph[nb][hv] = transpose8(hi);
+          pl[nb][hv] = transpose8(E::pack(a - r.x, b - r.y));
+        }
+      }
+      if (__any_sync(0xffffffffu, moved)) {
+#pragma unroll
+        for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+          for (int k = 0; k < D / 16; ++k)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) o[k][nb][e] *= alpha[nb][e & 1];
+      }
+      // hidden keys: P is 0, and V is cleared because 0 times what lies there
+      // need not be 0
+      uint32_t keep0 = 0xffffffffu, keep1 = 0xffffffffu;
+      if (!whole) {
+        const int kk = kw + tq * 2;
+        keep0 = (seen(kk) ? 0xffffu : 0u) | (seen(kk + 1) ? 0xffff0000u : 0u);
+        keep1 = (seen(kk + 8) ? 0xffffu : 0u) | (seen(kk + 9) ? 0xffff0000u : 0u);
+      }
+#pragma unroll
+      for (int k = 0; k < D / 16; ++k) {
+        uint32_t a[4];
+        ldsm4_t(a, tv + (k >> 2) * L::kSubBytes + row_v * 128 +
+                       ((((k & 3) * 2 + ((lane >> 3) & 1)) ^ (row_v & 7)) << 4));
+        a[0] &= keep0;
+        a[1] &= keep0;
+        a[2] &= keep1;
+        a[3] &= keep1;
+#pragma unroll
+        for (int nb = 0; nb < NB; ++nb) {
+          mma16816<E>(o[k][nb], a, ph[nb][0], ph[nb][1]);
+          mma16816<E>(o[k][nb], a, pl[nb][0], pl[nb][1]);
+        }
+      }
+    }
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&empty[st]);
+
+    const bool unit_end = w.t + 1 == sp.nt;
+    if (unit_end || i + 1 == n_tiles) {
+      // the four warps' results of this segment, joined
+#pragma unroll
+      for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          float x = l[nb][e];
+          x += __shfl_xor_sync(0xffffffffu, x, 4);
+          x += __shfl_xor_sync(0xffffffffu, x, 8);
+          x += __shfl_xor_sync(0xffffffffu, x, 16);
+          if (g == 0) {
+            const int hd = nb * 8 + tq * 2 + e;
+            ml[(warp * 8 * NB + hd) * 2] = ms[nb][e];
+            ml[(warp * 8 * NB + hd) * 2 + 1] = x;
+          }
+        }
+      named_bar_sync(1, 128);
+#pragma unroll
+      for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          const int hd = nb * 8 + tq * 2 + e;
+          float m = kNegInf;
+#pragma unroll
+          for (int v = 0; v < 4; ++v) m = fmaxf(m, ml[(v * 8 * NB + hd) * 2]);
+          const float f = ms[nb][e] == kNegInf ? 0.f : ex2(ms[nb][e] - m);
+#pragma unroll
+          for (int k = 0; k < D / 16; ++k) {
+            o[k][nb][e] *= f;
+            o[k][nb][e + 2] *= f;
+          }
+        }
+      const bool done = unit_end && seg_t0 == 0;       // the unit lies in this stretch
+      float* part = p.part + (size_t(blockIdx.x) * 2 + (first ? 0 : 1)) * (8 * NB * (D + 2));
+      const int hd = int(threadIdx.x) / (L::kJoinCols / 4);          // this thread's head and four columns
+      const int col = (int(threadIdx.x) % (L::kJoinCols / 4)) * 4;
+      float m = kNegInf, lsum = 0.f;
+#pragma unroll
+      for (int v = 0; v < 4; ++v) m = fmaxf(m, ml[(v * 8 * NB + hd) * 2]);
+#pragma unroll
+      for (int v = 0; v < 4; ++v) {
+        const float mv = ml[(v * 8 * NB + hd) * 2];
+        lsum += mv == kNegInf ? 0.f : ml[(v * 8 * NB + hd) * 2 + 1] * ex2(mv - m);
+      }
+#pragma unroll
+      for (int ch = 0; ch < D / L::kJoinCols; ++ch) {
+        constexpr int kPer = L::kJoinCols / 16;            // 16-wide pieces of d per round
+#pragma unroll
+        for (int k = 0; k < kPer; ++k)
+#pragma unroll
+          for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+              join[(warp * 8 * NB + nb * 8 + tq * 2 + (e & 1)) * L::kJoinRow + k * 16 + g + (e >> 1) * 8] =
+                  o[ch * kPer + k][nb][e];
+        named_bar_sync(1, 128);
+        float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+        for (int v = 0; v < 4; ++v) {
+          const float4 b = *reinterpret_cast<const float4*>(join + (v * 8 * NB + hd) * L::kJoinRow + col);
+          a.x += b.x;
+          a.y += b.y;
+          a.z += b.z;
+          a.w += b.w;
+        }
+        const int dd = ch * L::kJoinCols + col;
+        if (!done) {
+          *reinterpret_cast<float4*>(part + 16 * NB + hd * D + dd) = a;
+        } else if (hd < nh) {
+          const float inv = 1.f / lsum;
+          uint2 r;
+          r.x = E::pack(a.x * inv, a.y * inv);
+          r.y = E::pack(a.z * inv, a.w * inv);
+          *reinterpret_cast<uint2*>(static_cast<T*>(p.o) + (size_t(w.s) * p.H + h0 + hd) * D + dd) = r;
+        }
+        named_bar_sync(1, 128);
+      }
+      if (col == 0) {
+        if (!done) {
+          part[hd] = m;
+          part[8 * NB + hd] = lsum;
+        } else if (hd < nh) {
+          p.lse[size_t(w.s) * p.H + h0 + hd] = (m + lg2(lsum)) * kLn2;
+        }
+      }
+      fresh = true;
+      first = false;
+    }
+    if (i + 1 < n_tiles) w.next(cum, p.S, p.units);
+  }
+}
+
+// Puts a cut unit's partial results together: one CTA per (sequence, query
+// head); units that one CTA finished, and empty sequences, are left alone.
+// Thread t holds four elements of d and a quarter (d = 64: an eighth) of the
+// unit's pieces.
+template <int D, int NB, typename E>
+__global__ void __launch_bounds__(128) fa_decode_join_kernel(const DecodeParams p) {
+  using T = typename E::T;
+  constexpr float kLn2 = 0.69314718055994531f;
+  const float kNegInf = -__int_as_float(0x7f800000);
+  constexpr int kCols = D / 4, kRuns = 128 / kCols;
+  __shared__ float4 acc[128];
+  __shared__ float run_l[4], run_m[4];
+  grid_dep_wait();
+  grid_dep_launch();
+  const int s = blockIdx.x / p.H, h = blockIdx.x % p.H;
+  const int kvh = h / p.group, hg = h % p.group;
+  const int unit = kvh * p.blocks + hg / (8 * NB), hd = hg % (8 * NB);
+  const int c0 = p.cum[s], nt = p.cum[s + 1] - c0;
+  if (nt == 0) return;
+  const long long total = (long long)p.cum[p.S] * p.units;
+  const long long xa = (long long)c0 * p.units + (long long)unit * nt, xb = xa + nt;
+  const int ca = int(((xa + 1) * p.ctas - 1) / total), cb = int((xb * p.ctas - 1) / total);
+  if (ca == cb) return;                     // a whole unit in one stretch
+  const size_t slot = 8 * NB * (D + 2);
+  // the CTAs ca .. cb hold one piece each; only the first may begin before xa
+  auto piece = [&](int c) { return p.part + (size_t(c) * 2 + (dec_cut(total, p.ctas, c) >= xa ? 0 : 1)) * slot; };
+  auto has = [&](int c) { return dec_cut(total, p.ctas, c) < dec_cut(total, p.ctas, c + 1); };
+  // maximum and sum over the pieces
+  float m = kNegInf;
+  for (int c = ca + threadIdx.x; c <= cb; c += 128)
+    if (has(c)) m = fmaxf(m, piece(c)[hd]);
+#pragma unroll
+  for (int d = 16; d; d >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, d));
+  if (lane_id() == 0) run_m[warp_id()] = m;
+  __syncthreads();
+  m = fmaxf(fmaxf(run_m[0], run_m[1]), fmaxf(run_m[2], run_m[3]));
+  float l = 0.f;
+  for (int c = ca + threadIdx.x; c <= cb; c += 128)
+    if (has(c)) {
+      const float* x = piece(c);
+      l += x[hd] == kNegInf ? 0.f : x[8 * NB + hd] * ex2(x[hd] - m);
+    }
+#pragma unroll
+  for (int d = 16; d; d >>= 1) l += __shfl_xor_sync(0xffffffffu, l, d);
+  if (lane_id() == 0) run_l[warp_id()] = l;
+  const int dd = (threadIdx.x % kCols) * 4;
+  float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+  for (int c = ca + threadIdx.x / kCols; c <= cb; c += kRuns) {
+    if (!has(c)) continue;
+    const float* x = piece(c);
+    const float f = x[hd] == kNegInf ? 0.f : ex2(x[hd] - m);
+    const float4 b = *reinterpret_cast<const float4*>(x + 16 * NB + hd * D + dd);
+    a.x = fmaf(b.x, f, a.x);
+    a.y = fmaf(b.y, f, a.y);
+    a.z = fmaf(b.z, f, a.z);
+    a.w = fmaf(b.w, f, a.w);
+  }
+  acc[threadIdx.x] = a;
+  __syncthreads();
+  if (threadIdx.x < kCols) {
+#pragma unroll
+    for (int r = 1; r < kRuns; ++r) {
+      const float4 b = acc[threadIdx.x + r * kCols];
+      a.x += b.x;
+      a.y += b.y;
+      a.z += b.z;
+      a.w += b.w;
+    }
+    l = (run_l[0] + run_l[1]) + (run_l[2] + run_l[3]);
+    const float inv = 1.f / l;
+    uint2 r;
+    r.x = E::pack(a.x * inv, a.y * inv);
+    r.y = E::pack(a.z * inv, a.w * inv);
+    *reinterpret_cast<uint2*>(static_cast<T*>(p.o) + (size_t(s) * p.H + h) * D + dd) = r;
+    if (threadIdx.x == 0) p.lse[size_t(s) * p.H + h] = (m + lg2(l)) * kLn2;
+  }
+}
+
+}  // namespace fa

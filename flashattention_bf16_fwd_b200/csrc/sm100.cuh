@@ -11,7 +11,7 @@
 namespace fa {
 
 // Error codes a kernel leaves in the library's device flag.
-enum : int { kDevErrNone = 0, kDevErrTimeout = 1, kDevErrSmemAlign = 2 };
+enum : int { kDevErrNone = 0, kDevErrTimeout = 1, kDevErrSmemAlign = 2, kDevErrPages = 3 };
 
 // A bounded wait gives up after this long (ns of %globaltimer).
 constexpr uint64_t kWaitTimeoutNs = 4000000000ull;
