@@ -12,10 +12,10 @@ import sys
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
 LIB = os.path.join(PKG, "libfa_b200.so")
-SOURCES = [os.path.join(PKG, "csrc", f) for f in ("fa_api.cu", "fa_cache.cu")]
+SOURCES = [os.path.join(PKG, "csrc", f) for f in ("fa_api.cu", "fa_cache.cu", "fa_window.cu")]
 HEADERS = [os.path.join(PKG, "csrc", f) for f in ("sm100.cuh", "fa_fwd.cuh", "fa_bwd.cuh", "fa_selftest.cuh",
                                                   "fa_host.h", "fa_cache.cuh", "fa_decode.cuh")] + [
-    os.path.join(ROOT, "include", f) for f in ("fa_b200.h", "fa_b200_cache.h")]
+    os.path.join(ROOT, "include", f) for f in ("fa_b200.h", "fa_b200_cache.h", "fa_b200_window.h")]
 
 NVCC_FLAGS = [
     "-gencode", "arch=compute_100a,code=sm_100a",

@@ -11,6 +11,7 @@
 
 #include "../../include/fa_b200.h"
 #include "../../include/fa_b200_cache.h"
+#include "../../include/fa_b200_window.h"
 #include "fa_bwd.cuh"
 #include "fa_fwd.cuh"
 #include "fa_host.h"
@@ -109,60 +110,6 @@ DeviceState* device_state(int* why = nullptr) {
   DeviceState* var = device_state(&var##_why); \
   if (!var) return var##_why
 
-int check_common(int B, int H, int N, int d, int causal, float scale) {
-  if (d != 64 && d != 128) return FA_ERR_HEADDIM;
-  if (B < 1 || H < 1 || N < 1) return FA_ERR_SHAPE;
-  const long long total = (long long)B * H * N * d;
-  if (total >= (1ll << 31)) return FA_ERR_SHAPE;
-  if (causal != 0 && causal != 1) return FA_ERR_ARG;
-  if (!std::isfinite(scale) || !(scale > 0.f)) return FA_ERR_ARG;
-  return FA_OK;
-}
-
-// A [BH, N, D] bf16 tensor seen as 3-D (d, n, bh); boxes of 64 x box_rows x 1
-// (128 for the loads the tcgen05 descriptors read, 32 for the forward's O
-// stores, one per warp) with the 128-byte swizzle.  Loads read 0 past N; stores
-// drop rows past N.
-bool make_map(CUtensorMap* map, const void* base, int BH, int N, int D,
-              CUtensorMapDataType dt = CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, unsigned box_rows = 128) {
-  PFN_cuTensorMapEncodeTiled_v12000 enc = encoder();
-  if (!enc) return false;
-  cuuint64_t dims[3] = {cuuint64_t(D), cuuint64_t(N), cuuint64_t(BH)};
-  cuuint64_t strides[2] = {cuuint64_t(D) * 2, cuuint64_t(N) * D * 2};
-  cuuint32_t box[3] = {64, box_rows, 1};
-  cuuint32_t estr[3] = {1, 1, 1};
-  return enc(map, dt, 3, const_cast<void*>(base), dims, strides, box, estr,
-             CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
-}
-
-// The FP32 dQ accumulator [BH, N, D] as 3-D (d, n, bh) with 32 x 32 boxes and
-// the 128-byte swizzle, for TMA reduce-add.
-bool make_map_dq(CUtensorMap* map, const void* base, int BH, int N, int D) {
-  PFN_cuTensorMapEncodeTiled_v12000 enc = encoder();
-  if (!enc) return false;
-  cuuint64_t dims[3] = {cuuint64_t(D), cuuint64_t(N), cuuint64_t(BH)};
-  cuuint64_t strides[2] = {cuuint64_t(D) * 4, cuuint64_t(N) * D * 4};
-  cuuint32_t box[3] = {32, 32, 1};
-  cuuint32_t estr[3] = {1, 1, 1};
-  return enc(map, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 3, const_cast<void*>(base), dims, strides, box, estr,
-             CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
-}
-
-// Shift added to m on repeated-max rows (base-2 units): maps a maximum to 1 - 2^-8.
-const double kDeltaLog2 = -std::log2(1.0 - 1.0 / 256.0);
-// The same for fp16 P_bar: maps a maximum to 1 - 2^-11.
-const double kDeltaLog2F16 = -std::log2(1.0 - 1.0 / 2048.0);
-
-template <typename E>
-constexpr CUtensorMapDataType map_type() {
-  return E::kMmaFmt == 1 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16;
-}
-
-// H query heads share Hkv key/value heads (H == Hkv: ordinary attention).
-int check_heads(int H, int Hkv) { return (Hkv >= 1 && Hkv <= H && H % Hkv == 0) ? FA_OK : FA_ERR_SHAPE; }
-
 template <typename E>
 int launch_fwd(const void* q, const void* k, const void* v, void* o, float* lse, int32_t* ties, int32_t* one_hit,
                float* o_f32, int B, int H, int Hkv, int N, int d, int causal, float scale, int fix_mode,
@@ -195,18 +142,7 @@ int launch_fwd(const void* q, const void* k, const void* v, void* o, float* lse,
   prm.n_pairs = (N + 255) / 256;
   prm.causal = causal;
   prm.scale_log2 = float(double(scale) * 1.4426950408889634);
-  // shift on repeated-max rows per fix_mode, in base-2 units: 1 and 5 map the
-  // maxima to the largest value below 1 of the P_bar format (1 - 2^-8 in bf16,
-  // 1 - 2^-11 in fp16), 2 to 0.5, 3 to exp(-1/16); 0 and 4 keep the plain shift
-  const double delta = (fix_mode == 1 || fix_mode == 5) ? (kF16 ? kDeltaLog2F16 : kDeltaLog2)
-                       : fix_mode == 2                  ? 1.0
-                       : fix_mode == 3                  ? 1.4426950408889634 / 16.0
-                                                        : 0.0;
-  prm.delta_log2 = float(delta);
-  prm.fix_factor = float(std::exp2(-delta));
-  prm.fix = (fix_mode == 1 || fix_mode == 2 || fix_mode == 3 || fix_mode == 5) ? 1 : 0;
-  prm.self_norm = (fix_mode == 4) ? 1 : 0;
-  prm.near = (fix_mode == 5) ? 1 : 0;
+  set_fix(prm, fix_mode, kF16);
   const int n_items = prm.n_pairs * BH;
   const dim3 grid(unsigned(n_items < st->num_sms ? n_items : st->num_sms));
   // self-normalised or near-tie code, or a debug record
@@ -217,8 +153,6 @@ int launch_fwd(const void* q, const void* k, const void* v, void* o, float* lse,
   const cudaError_t e = launch(kern, grid, dim3(FwdLayout<64>::kThreads), smem, stream, mq, mk, mv, mo, prm);
   return e == cudaSuccess ? FA_OK : FA_ERR_LAUNCH;
 }
-
-size_t align256(size_t x) { return (x + 255) & ~size_t(255); }
 
 }  // namespace
 
@@ -468,6 +402,7 @@ const char* fa_status_string(int status) {
     case FA_ERR_CACHE_SHAPE:
       return "a cache argument is out of range: the page size, the number of pages, sequences or tokens, a row "
              "stride, or the window";
+    case FA_ERR_WINDOW: return "window must be at least 1 and sinks at least 0";
     default: return "unknown status";
   }
 }

@@ -16,6 +16,8 @@
 // fa_bwd_kernel roles and TMEM use are described above the kernel.
 #pragma once
 
+#include <type_traits>
+
 #include "sm100.cuh"
 
 namespace fa {
@@ -78,6 +80,52 @@ __global__ void __launch_bounds__(256) fa_bwd_dq_kernel(const float* __restrict_
   reinterpret_cast<uint4*>(dq)[i] = w;
 }
 
+// The windowed backward's last launch: dQ = scale * accumulator as above (the
+// first `dq_blocks` blocks), and the sink rows of split key tiles as the sum of
+// their pieces, in order (one thread per row, dK or dV, and four columns).
+// part: [BH][pieces][rows][dK, dV][d]; dk, dv: [BH][N][d].
+template <typename E>
+__global__ void __launch_bounds__(256)
+    fa_bwd_window_finish_kernel(const float* __restrict__ acc, typename E::T* __restrict__ dq, float scale,
+                                long long n8, unsigned dq_blocks, const float* __restrict__ part,
+                                typename E::T* __restrict__ dk, typename E::T* __restrict__ dv, int pieces, int rows,
+                                int N, int d, long long part_items) {
+  grid_dep_wait();
+  grid_dep_launch();
+  if (blockIdx.x < dq_blocks) {
+    const long long i = (long long)blockIdx.x * blockDim.x + threadIdx.x;
+    if (i >= n8) return;
+    const float4 a = reinterpret_cast<const float4*>(acc)[2 * i];
+    const float4 b = reinterpret_cast<const float4*>(acc)[2 * i + 1];
+    uint4 w;
+    w.x = E::pack(a.x * scale, a.y * scale);
+    w.y = E::pack(a.z * scale, a.w * scale);
+    w.z = E::pack(b.x * scale, b.y * scale);
+    w.w = E::pack(b.z * scale, b.w * scale);
+    reinterpret_cast<uint4*>(dq)[i] = w;
+    return;
+  }
+  const long long i = (long long)(blockIdx.x - dq_blocks) * blockDim.x + threadIdx.x;
+  if (i >= part_items) return;
+  const int per_row = d / 2;                             // dK and dV, four columns each
+  const int c = int(i % per_row);
+  const long long row = i / per_row;                     // (head, key)
+  const long long bh = row / rows;
+  const int key = int(row % rows);
+  const float* x = part + (bh * pieces * rows + key) * 2 * d + 4 * c;
+  float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
+  for (int s = 0; s < pieces; ++s) {
+    const float4 b = *reinterpret_cast<const float4*>(x + (long long)s * rows * 2 * d);
+    a.x += b.x;
+    a.y += b.y;
+    a.z += b.z;
+    a.w += b.w;
+  }
+  const bool is_v = 4 * c >= d;
+  typename E::T* out = (is_v ? dv : dk) + (bh * N + key) * d + (4 * c - (is_v ? d : 0));
+  *reinterpret_cast<uint2*>(out) = make_uint2(E::pack(a.x, a.y), E::pack(a.z, a.w));
+}
+
 struct BwdParams {
   const float* lse;     // [BH, N] natural log
   const float* dsum;    // [BH, N] D_i
@@ -89,6 +137,12 @@ struct BwdParams {
   int H, group;         // query heads per batch entry; query heads per K/V head (1 = no sharing)
   float scale, scale_log2;
   int after_pre;        // 1: launched right after fa_bwd_pre_kernel on the same stream
+  // windowed kernel (BwdWindow)
+  int window, sinks;    // key j is visible where j <= i and (i - j < window or j < sinks)
+  int near;             // query tiles whose window reaches a key tile
+  int split, chunks, chunk;   // key tiles with a far part; its pieces, and their query tiles
+  float* part;          // [BH][1 + chunks][part_rows][dK, dV][D]: pieces of the split tiles' sink rows
+  int part_rows;
 };
 
 template <int D>
@@ -143,10 +197,12 @@ struct BwdLayout {
 // shares the K/V head (dK, dV accumulate over all of them): n_it steps.
 struct BwdItem {
   int bh, kv_tile, key0, i_start, n_it_head, n_it;
+  int piece;            // windowed kernel: -1, or which piece of a split key tile (0: its window)
 };
 
 __device__ __forceinline__ BwdItem bwd_item_at(const BwdParams& p, int bh, int kv_tile) {
   BwdItem w;
+  w.piece = -1;
   w.bh = bh;
   w.kv_tile = kv_tile;
   w.key0 = kv_tile * 128;
@@ -198,6 +254,49 @@ struct BwdSched {
   }
 };
 
+// The windowed kernel's items.  A key tile is seen by `near` query tiles, from
+// its own on; one that holds sinks is seen by every later query tile too.  As
+// one item it would take N / 128 steps where the others take `near`, and the
+// CTAs that drew such an item would finish long after the rest (H = 32 over
+// Hkv = 8, N = 8192, window 1024: 256 steps against 135 on average).  So the far
+// part is cut into pieces of `chunk` query tiles, items of their own, which
+// leave FP32 dK and dV of the sink rows; fa_bwd_window_finish_kernel adds the
+// pieces in a fixed order.  The far pieces come first, then the key tiles, head
+// by head: neighbours share their queries in the L2.
+struct BwdWindow {
+  int rnd, item, n_far, n_items;
+  __device__ __forceinline__ explicit BwdWindow(const BwdParams& p) : rnd(0), item(snake_item(0)) {
+    n_far = p.split * p.chunks * p.BH;
+    n_items = n_far + p.n_kv * p.BH;
+  }
+  __device__ __forceinline__ bool valid() const { return item < n_items; }
+  __device__ __forceinline__ BwdItem get(const BwdParams& p) const {
+    BwdItem w;
+    const int n_q = p.n_kv;
+    int end;
+    if (item < n_far) {
+      const int c = item / p.BH % p.chunks;
+      w.bh = item % p.BH;
+      w.kv_tile = item / p.BH / p.chunks;
+      w.piece = 1 + c;
+      w.i_start = max(w.kv_tile + p.near, p.near + c * p.chunk);
+      end = min(n_q, p.near + (c + 1) * p.chunk);
+    } else {
+      const int i = item - n_far;
+      w.bh = i / p.n_kv;
+      w.kv_tile = i % p.n_kv;
+      w.piece = w.kv_tile < p.split ? 0 : -1;
+      w.i_start = w.kv_tile;
+      end = min(n_q, w.kv_tile + p.near);
+    }
+    w.key0 = w.kv_tile * 128;
+    w.n_it_head = end - w.i_start;
+    w.n_it = w.n_it_head * p.group;
+    return w;
+  }
+  __device__ __forceinline__ void next(const BwdParams&) { item = snake_item(++rnd); }
+};
+
 // The steps of an item in order: query tile qt of batch*query-head bh_q,
 // query tiles innermost.  Advanced once per step, without divisions.
 struct BwdSteps {
@@ -236,13 +335,15 @@ struct BwdSteps {
 // re-initialisation: `g` counts query-tile steps, `n_done` counts items.
 // E: the element format (ElemBF16 or ElemF16) of Q, K, V, dO, dK, dV and of
 // the P_bar and dS operands.  kPairs: the head-major pair schedule (BwdSched).
-template <int D, typename E = ElemBF16, bool kPairs = false>
+// kWin: the windowed kernel (BwdWindow's items, and the window's mask).
+template <int D, typename E = ElemBF16, bool kPairs = false, bool kWin = false>
 __global__ void __launch_bounds__(512, 1)
     fa_bwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
                   const __grid_constant__ CUtensorMap tm_v, const __grid_constant__ CUtensorMap tm_do,
                   const __grid_constant__ CUtensorMap tm_dq, const __grid_constant__ CUtensorMap tm_dk,
                   const __grid_constant__ CUtensorMap tm_dv, const BwdParams p) {
   using L = BwdLayout<D>;
+  using Sched = std::conditional_t<kWin, BwdWindow, BwdSched<kPairs>>;
   extern __shared__ __align__(1024) uint8_t smem[];
   uint64_t* bars = reinterpret_cast<uint64_t*>(smem + L::kBarOff);
   uint64_t* kv_full = bars;        // [2]
@@ -334,7 +435,7 @@ __global__ void __launch_bounds__(512, 1)
       uint32_t n_done = 0;   // items started
       bool ok = true;
       bool dep_done = false;
-      for (BwdSched<kPairs> sc(p); ok && sc.valid(); sc.next(p), ++n_done) {
+      for (Sched sc(p); ok && sc.valid(); sc.next(p), ++n_done) {
         const BwdItem w = sc.get(p);
         const uint32_t ks = n_done % L::kKVStages;
         ok = __all_sync(0xffffffffu, mbar_wait(&kv_empty[ks], ((n_done / L::kKVStages) & 1) ^ 1, wd));
@@ -384,7 +485,7 @@ __global__ void __launch_bounds__(512, 1)
       const uint64_t pol_q = l2_policy_evict_last();
       uint32_t g = 0;
       bool ok = true;
-      for (BwdSched<kPairs> sc(p); ok && sc.valid(); sc.next(p)) {
+      for (Sched sc(p); ok && sc.valid(); sc.next(p)) {
         const BwdItem w = sc.get(p);
         BwdSteps sp(p, w);
         for (int it = 0; it < w.n_it; ++it, ++g, sp.next()) {
@@ -450,12 +551,12 @@ __global__ void __launch_bounds__(512, 1)
         // are issued during this item's last step (as within an item), so
         // the compute warps do not wait for them at the item boundary
         bool first_issued = false;
-        for (BwdSched<kPairs> sc(p); ok && sc.valid(); sc.next(p), ++n_done) {
+        for (Sched sc(p); ok && sc.valid(); sc.next(p), ++n_done) {
           const BwdItem w = sc.get(p);
           const uint32_t ks = n_done % L::kKVStages;
           const uint32_t sk = k_of(n_done);
           const uint32_t sv = sk + (L::kTileBytes >> 4);
-          BwdSched<kPairs> nx = sc;
+          Sched nx = sc;
           nx.next(p);
           const bool prefetch_next = !L::kWide && nx.valid();
           const uint32_t nsk = k_of(n_done + 1);
@@ -554,7 +655,7 @@ __global__ void __launch_bounds__(512, 1)
     const uint64_t c2 = f2_pack(p.scale_log2, p.scale_log2);
     uint32_t g = 0;
     bool ok = true;
-    for (BwdSched<kPairs> sc(p); ok && sc.valid(); sc.next(p)) {
+    for (Sched sc(p); ok && sc.valid(); sc.next(p)) {
       const BwdItem w = sc.get(p);
       const bool key_in = w.key0 + kr < p.N;
       BwdSteps sp(p, w);
@@ -570,6 +671,14 @@ __global__ void __launch_bounds__(512, 1)
         tc_fence_after();
         // P^T: P[q] = 2^(S*scale_log2 - LSE2[q]); masked entries are 0
         uint32_t pk[32];
+        [[maybe_unused]] float pf[kWin ? 64 : 1];      // windowed kernel: P before its rounding
+        auto pack_p = [&](int i, float p0, float p1) {
+          pk[i] = E::pack(p0, p1);
+          if constexpr (kWin) {
+            pf[2 * i] = p0;
+            pf[2 * i + 1] = p1;
+          }
+        };
         {
           uint32_t r[2][32];
           tmem_ld32(t_s, r[0]);
@@ -577,7 +686,11 @@ __global__ void __launch_bounds__(512, 1)
           tmem_ld_wait(r[0]);
           tmem_ld_wait(r[1]);
           const bool diag = p.causal && qt == w.kv_tile;
-          if (!__any_sync(0xffffffffu, !key_in || diag)) {   // no masked entry in this warp
+          // windowed kernel: queries from `far` of this half on do not see the key
+          int far = 64;
+          if constexpr (kWin)
+            if (w.key0 + kr >= p.sinks) far = min(64, w.key0 + kr + p.window - qt * 128 - 64 * half);
+          if (!__any_sync(0xffffffffu, !key_in || diag || (kWin && far < 64))) {   // no masked entry in this warp
 #pragma unroll
             for (int j = 0; j < 16; ++j) {             // 4 queries per shared-memory load of -LSE2
               const float4 nl = *reinterpret_cast<const float4*>(nlse + 4 * j);
@@ -589,7 +702,7 @@ __global__ void __launch_bounds__(512, 1)
                                          __uint_as_float(r[i >> 4][(2 * i + 1) & 31])),
                                  c2, h ? f2_pack(nl.z, nl.w) : f2_pack(nl.x, nl.y)),
                           x0, x1);
-                pk[i] = E::pack(ex2(x0), ex2(x1));
+                pack_p(i, ex2(x0), ex2(x1));
               }
             }
           } else {
@@ -611,7 +724,11 @@ __global__ void __launch_bounds__(512, 1)
                           x0, x1);
                 x0 = (2 * i < lim) ? -__int_as_float(0x7f800000) : x0;
                 x1 = (2 * i + 1 < lim) ? -__int_as_float(0x7f800000) : x1;
-                pk[i] = E::pack(ex2(x0), ex2(x1));
+                if constexpr (kWin) {
+                  x0 = (2 * i >= far) ? -__int_as_float(0x7f800000) : x0;
+                  x1 = (2 * i + 1 >= far) ? -__int_as_float(0x7f800000) : x1;
+                }
+                pack_p(i, ex2(x0), ex2(x1));
               }
             }
           }
@@ -634,46 +751,80 @@ __global__ void __launch_bounds__(512, 1)
 
         if (!(ok = __all_sync(0xffffffffu, mbar_wait(dp_full, g & 1, wd)))) break;
         tc_fence_after();
-        // dS^T = P_bar * (dP - D[q])
-        uint32_t dsw[32];
-        {
-          uint32_t r[2][32];
-          tmem_ld32(t_dp, r[0]);
-          tmem_ld32(t_dp + 32, r[1]);
-          tmem_ld_wait(r[0]);
-          tmem_ld_wait(r[1]);
+        if constexpr (kWin) {
+          // dS^T = P * (dP - D[q]) with P unrounded (a rounded P adds its error to
+          // that of dS's own rounding: dQ and dK are 2.0 times a half step off
+          // instead of 1.4), 32 queries at a time to stay within the registers
 #pragma unroll
-          for (int j = 0; j < 16; ++j) {               // 4 queries per shared-memory load of D
-            const float4 d4 = *reinterpret_cast<const float4*>(dd + 4 * j);
+          for (int c = 0; c < 2; ++c) {
+            uint32_t r[32], wv[16];
+            tmem_ld32(t_dp + 32 * c, r);
+            tmem_ld_wait(r);
 #pragma unroll
-            for (int h = 0; h < 2; ++h) {
-              const int i = 2 * j + h;
-              const float2 pp = E::unpack(pk[i]);
-              const uint64_t dq2 = h ? f2_pack(d4.z, d4.w) : f2_pack(d4.x, d4.y);
-              const uint64_t dp2 = f2_pack(__uint_as_float(r[i >> 4][(2 * i) & 31]),
-                                           __uint_as_float(r[i >> 4][(2 * i + 1) & 31]));
-              float y0, y1;
-              f2_unpack(f2_mul(f2_fma(dq2, f2_pack(-1.f, -1.f), dp2), f2_pack(pp.x, pp.y)), y0, y1);
-              dsw[i] = E::pack(y0, y1);
+            for (int j = 0; j < 8; ++j) {
+              const float4 d4 = *reinterpret_cast<const float4*>(dd + 32 * c + 4 * j);
+#pragma unroll
+              for (int h = 0; h < 2; ++h) {
+                const int i = 2 * j + h;
+                const uint64_t dq2 = h ? f2_pack(d4.z, d4.w) : f2_pack(d4.x, d4.y);
+                const uint64_t dp2 = f2_pack(__uint_as_float(r[2 * i]), __uint_as_float(r[2 * i + 1]));
+                float y0, y1;
+                f2_unpack(f2_mul(f2_fma(dq2, f2_pack(-1.f, -1.f), dp2),
+                                 f2_pack(pf[32 * c + 2 * i], pf[32 * c + 2 * i + 1])),
+                          y0, y1);
+                wv[i] = E::pack(y0, y1);
+              }
+            }
+            // dS of these queries takes columns 16 c to 16 c + 15, whose dP has
+            // been read
+            tmem_st16(t_dp + 16 * c, wv);
+#pragma unroll
+            for (int c16 = 0; c16 < 4; ++c16)
+              *reinterpret_cast<uint4*>(ds_row + (((4 * c + c16) ^ (kr & 7)) << 4)) =
+                  make_uint4(wv[c16 * 4], wv[c16 * 4 + 1], wv[c16 * 4 + 2], wv[c16 * 4 + 3]);
+          }
+        } else {
+          // dS^T = P_bar * (dP - D[q])
+          uint32_t dsw[32];
+          {
+            uint32_t r[2][32];
+            tmem_ld32(t_dp, r[0]);
+            tmem_ld32(t_dp + 32, r[1]);
+            tmem_ld_wait(r[0]);
+            tmem_ld_wait(r[1]);
+#pragma unroll
+            for (int j = 0; j < 16; ++j) {               // 4 queries per shared-memory load of D
+              const float4 d4 = *reinterpret_cast<const float4*>(dd + 4 * j);
+#pragma unroll
+              for (int h = 0; h < 2; ++h) {
+                const int i = 2 * j + h;
+                const float2 pp = E::unpack(pk[i]);
+                const uint64_t dq2 = h ? f2_pack(d4.z, d4.w) : f2_pack(d4.x, d4.y);
+                const uint64_t dp2 = f2_pack(__uint_as_float(r[i >> 4][(2 * i) & 31]),
+                                             __uint_as_float(r[i >> 4][(2 * i + 1) & 31]));
+                float y0, y1;
+                f2_unpack(f2_mul(f2_fma(dq2, f2_pack(-1.f, -1.f), dp2), f2_pack(pp.x, pp.y)), y0, y1);
+                dsw[i] = E::pack(y0, y1);
+              }
             }
           }
-        }
-        {
-          uint32_t wv[16];
+          {
+            uint32_t wv[16];
 #pragma unroll
-          for (int i = 0; i < 16; ++i) wv[i] = dsw[i];
-          tmem_st16(t_dp, wv);
+            for (int i = 0; i < 16; ++i) wv[i] = dsw[i];
+            tmem_st16(t_dp, wv);
 #pragma unroll
-          for (int i = 0; i < 16; ++i) wv[i] = dsw[16 + i];
-          tmem_st16(t_dp + 16, wv);
-        }
-        // dS into shared memory for dQ = dS K: MN-major, 128-byte swizzle.
-        // dQ of the previous step, its last reader, was issued before this
-        // step's dP^T, so dp_full already implied that it is done.
+            for (int i = 0; i < 16; ++i) wv[i] = dsw[16 + i];
+            tmem_st16(t_dp + 16, wv);
+          }
+          // dS into shared memory for dQ = dS K: MN-major, 128-byte swizzle.
+          // dQ of the previous step, its last reader, was issued before this
+          // step's dP^T, so dp_full already implied that it is done.
 #pragma unroll
-        for (int c16 = 0; c16 < 8; ++c16) {
-          uint4* dst = reinterpret_cast<uint4*>(ds_row + ((c16 ^ (kr & 7)) << 4));
-          *dst = make_uint4(dsw[c16 * 4], dsw[c16 * 4 + 1], dsw[c16 * 4 + 2], dsw[c16 * 4 + 3]);
+          for (int c16 = 0; c16 < 8; ++c16) {
+            uint4* dst = reinterpret_cast<uint4*>(ds_row + ((c16 ^ (kr & 7)) << 4));
+            *dst = make_uint4(dsw[c16 * 4], dsw[c16 * 4 + 1], dsw[c16 * 4 + 2], dsw[c16 * 4 + 3]);
+          }
         }
         fence_proxy_async_smem();
         tmem_st_wait();
@@ -694,7 +845,7 @@ __global__ void __launch_bounds__(512, 1)
     uint32_t g = 0;
     uint32_t n_done = 0;
     bool ok = true;
-    for (BwdSched<kPairs> sc(p); ok && sc.valid(); sc.next(p), ++n_done) {
+    for (Sched sc(p); ok && sc.valid(); sc.next(p), ++n_done) {
       const BwdItem w = sc.get(p);
       BwdSteps sp(p, w);
       for (int it = 0; it < w.n_it; ++it, ++g, sp.next()) {
@@ -741,7 +892,45 @@ __global__ void __launch_bounds__(512, 1)
       if (!ok) break;
       tc_fence_after();
       const int key = w.key0 + rr;
-      if constexpr (D == 64) {
+      if (kWin && w.piece >= 0) {
+        // a piece of a split key tile: FP32 sums of the sink rows; the other rows
+        // are seen by the window alone and are final
+        const bool sink = key < p.part_rows;
+        float* part = p.part + ((size_t(w.bh) * (1 + p.chunks) + w.piece) * p.part_rows + key) * (2 * D);
+        for (int which = 0; which < 2; ++which) {
+          const uint32_t t_src = tmem + lane_base + (which ? L::kTmDK : L::kTmDV);
+          const float mul = which ? p.scale : 1.f;
+          uint4* dst = reinterpret_cast<uint4*>(static_cast<typename E::T*>(which ? p.dk : p.dv) +
+                                                (size_t(w.bh) * p.N + key) * D);
+          float4* dstf = reinterpret_cast<float4*>(part + (which ? 0 : D));
+#pragma unroll 1
+          for (int c = 0; c < D / 32; ++c) {
+            uint32_t r[32];
+            tmem_ld32(t_src + c * 32, r);
+            tmem_ld_wait(r);
+#pragma unroll
+            for (int i = 0; i < 32; ++i) r[i] = __float_as_uint(__uint_as_float(r[i]) * mul);
+            if (sink) {
+#pragma unroll
+              for (int i = 0; i < 8; ++i)
+                dstf[c * 8 + i] = make_float4(__uint_as_float(r[4 * i]), __uint_as_float(r[4 * i + 1]),
+                                              __uint_as_float(r[4 * i + 2]), __uint_as_float(r[4 * i + 3]));
+            } else if (w.piece == 0 && key < p.N) {
+#pragma unroll
+              for (int i = 0; i < 4; ++i) {
+                uint4 v;
+                v.x = E::pack(__uint_as_float(r[8 * i]), __uint_as_float(r[8 * i + 1]));
+                v.y = E::pack(__uint_as_float(r[8 * i + 2]), __uint_as_float(r[8 * i + 3]));
+                v.z = E::pack(__uint_as_float(r[8 * i + 4]), __uint_as_float(r[8 * i + 5]));
+                v.w = E::pack(__uint_as_float(r[8 * i + 6]), __uint_as_float(r[8 * i + 7]));
+                dst[c * 4 + i] = v;
+              }
+            }
+          }
+        }
+        tc_fence_before();
+        mbar_arrive(dkv_free);                       // the next item may overwrite dK, dV
+      } else if constexpr (D == 64) {
         // dV and dK through this warp's two staging boxes (32 rows each, the
         // 128-byte swizzle) and one TMA store box each; rows past N are
         // dropped by the tensor maps.  dV goes into the box the next dQ drain

@@ -15,7 +15,6 @@ namespace {
 constexpr int kMaxDevices = 64;
 
 bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
-size_t align256(size_t x) { return (x + 255) & ~size_t(255); }
 
 int check_cache(int S, int Hkv, int d, int P, int page, int M) {
   if (d != 64 && d != 128) return FA_ERR_HEADDIM;
@@ -45,21 +44,6 @@ CacheParams cache_params(void* k_pages, void* v_pages, int32_t* refs, int32_t* t
   p.hkv = Hkv;
   p.row_log2 = d == 64 ? 3 : 4;
   return p;
-}
-
-// One layer of the cache as a 3-D tensor (d, token of the page, page and head);
-// boxes of 64 elements x `box` tokens with the 128-byte swizzle.
-bool make_page_map(CUtensorMap* map, const void* base, int P, int Hkv, int page, int d, int box, bool bf16) {
-  PFN_cuTensorMapEncodeTiled_v12000 enc = encoder();
-  if (!enc) return false;
-  cuuint64_t dims[3] = {cuuint64_t(d), cuuint64_t(page), cuuint64_t(P) * Hkv};
-  cuuint64_t strides[2] = {cuuint64_t(d) * 2, cuuint64_t(page) * d * 2};
-  cuuint32_t boxes[3] = {64, cuuint32_t(box), 1};
-  cuuint32_t estr[3] = {1, 1, 1};
-  return enc(map, bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 3,
-             const_cast<void*>(base), dims, strides, boxes, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
-             CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
 // Large shared memory for the kernels that may need it, once per device.
@@ -103,9 +87,10 @@ int decode_nb(int group) { return group > 8 ? 2 : 1; }
 template <int D, int NB, typename E>
 int launch_decode(const void* k_pages, const void* v_pages, DecodeParams prm, int Hkv, cudaStream_t stream) {
   CUtensorMap mk, mv;
-  constexpr bool bf16 = E::kMmaFmt == 1;
-  if (!make_page_map(&mk, k_pages, prm.P, Hkv, prm.page, D, prm.box, bf16) ||
-      !make_page_map(&mv, v_pages, prm.P, Hkv, prm.page, D, prm.box, bf16))
+  // one layer of the cache: (d, token of the page, page and head), boxes of 64 x box
+  constexpr CUtensorMapDataType dt = map_type<E>();
+  if (!make_map(&mk, k_pages, prm.P * Hkv, prm.page, D, dt, prm.box) ||
+      !make_map(&mv, v_pages, prm.P * Hkv, prm.page, D, dt, prm.box))
     return FA_ERR_DEVICE;
   if (launch(fa_decode_kernel<D, NB, E>, dim3(prm.ctas), dim3(DecLayout<D, NB>::kThreads),
              DecLayout<D, NB>::bytes(prm.S), stream, mk, mv, prm) != cudaSuccess)

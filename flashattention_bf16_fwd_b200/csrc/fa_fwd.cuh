@@ -61,6 +61,7 @@ struct FwdParams {
   int fix;              // raise the shift on repeated-max rows
   int self_norm;        // divide O by the sum of the rounded P_bar instead of the unrounded P
   int near;             // detect near ties (P rounds to 1.0 in the element format) instead of exact ties of S
+  int window, sinks;    // windowed kernel: key j is visible where j <= i and (i - j < window or j < sinks)
 };
 
 template <int D>
@@ -104,10 +105,36 @@ struct FwdLayout {
 // measured slower: the balance of the heavy-first order matters more.)
 struct FwdItem {
   int bh, q0_row, n0, n1, nmax;
+  // windowed kernel: the item's key tiles are those with a sink, then, `gap`
+  // tiles on, those from the first query tile's window to the last diagonal
+  // tile.  Query tile 0 takes the first n0 of them; query tile 1 takes all but
+  // number skip1, which only query tile 0 sees (-1: it sees them all).
+  int sink_tiles, gap, skip1;
 };
 
-__device__ __forceinline__ FwdItem fwd_item(const FwdParams& p, int item) {
+// The key tile that is number j of a windowed item.
+__device__ __forceinline__ int fwd_key_tile(const FwdItem& w, int j) { return j < w.sink_tiles ? j : j + w.gap; }
+
+__device__ __forceinline__ FwdItem fwd_window_item(const FwdParams& p, int item) {
   FwdItem it;
+  const int pair = p.n_pairs - 1 - item / p.BH;
+  it.bh = item % p.BH;
+  it.q0_row = pair * 256;
+  const bool second = it.q0_row + 128 < p.N;
+  const int a0 = max(0, it.q0_row - p.window + 1) >> 7;          // first tile of each query tile's window
+  const int a1 = max(0, it.q0_row + 129 - p.window) >> 7;
+  const int last = 2 * pair + (second ? 1 : 0);                  // the last diagonal tile
+  it.sink_tiles = min((min(p.sinks, p.N) + 127) >> 7, last + 1);
+  it.gap = max(0, a0 - it.sink_tiles);
+  it.nmax = last + 1 - it.gap;
+  it.n0 = 2 * pair + 1 - it.gap;
+  it.n1 = second ? it.nmax : 0;
+  it.skip1 = (a1 > a0 && a0 >= it.sink_tiles) ? it.sink_tiles : -1;
+  return it;
+}
+
+__device__ __forceinline__ FwdItem fwd_item(const FwdParams& p, int item) {
+  FwdItem it{};
   const int pair = p.causal ? (p.n_pairs - 1 - item / p.BH) : item / p.BH;
   it.bh = item % p.BH;
   it.q0_row = pair * 256;
@@ -138,7 +165,9 @@ __device__ __forceinline__ constexpr float rounds_to_one() {
 // (near ties) and with the debug records (tie record, P_bar == 1 count, O
 // before rounding); the other instantiation, used for fix_mode 0-3 without
 // records, leaves all of it out.
-template <int D, bool kVariants, typename E = ElemBF16>
+// kWin: the windowed kernel, in which each query sees the keys of its window and
+// the sinks: the same pipeline over a shorter list of key tiles.
+template <int D, bool kVariants, typename E = ElemBF16, bool kWin = false>
 __global__ void __launch_bounds__(384, 1)
     fa_fwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
                   const __grid_constant__ CUtensorMap tm_v, const __grid_constant__ CUtensorMap tm_o,
@@ -206,6 +235,16 @@ __global__ void __launch_bounds__(384, 1)
   grid_dep_wait();
   grid_dep_launch();
   const Watchdog wd{abort_flag, p.dev_error};
+  auto get_item = [&](int i) {
+    if constexpr (kWin)
+      return fwd_window_item(p, i);
+    else
+      return fwd_item(p, i);
+  };
+  // windowed kernel: does query tile qt of the item take key tile number j?
+  auto takes = [](const FwdItem& w, int qt, int j) {
+    return j < (qt ? w.n1 : w.n0) && !(qt && j == w.skip1);
+  };
 
   if (warp >= 8) {
     // Producer and MMA warps need few registers; give them back first.
@@ -219,7 +258,7 @@ __global__ void __launch_bounds__(384, 1)
         uint32_t n_done = 0;   // items started
         bool ok = true;
         for (int rnd = 0, item = snake_item(0); ok && item < n_items; item = snake_item(++rnd), ++n_done) {
-          const FwdItem w = fwd_item(p, item);
+          const FwdItem w = get_item(item);
           // grouped-query layout: query head h reads K/V head h / group
           const int kv_bh = (w.bh / p.H) * (p.H / p.group) + (w.bh % p.H) / p.group;
           // the S MMAs of the item kQBufs back must be done with this Q buffer
@@ -237,9 +276,10 @@ __global__ void __launch_bounds__(384, 1)
             mbar_arrive_expect_tx(&kv_full[st], uint32_t(2 * L::kTileBytes));
             uint8_t* sk = smem + L::kKVOff + st * 2 * L::kTileBytes;
             uint8_t* sv = sk + L::kTileBytes;
+            const int key0 = (kWin ? fwd_key_tile(w, j) : j) * 128;
             for (int s = 0; s < L::kSub; ++s) {
-              tma_load_3d(sk + s * L::kSubBytes, &tm_k, &kv_full[st], s * 64, j * 128, kv_bh, pol_kv);
-              tma_load_3d(sv + s * L::kSubBytes, &tm_v, &kv_full[st], s * 64, j * 128, kv_bh, pol_kv);
+              tma_load_3d(sk + s * L::kSubBytes, &tm_k, &kv_full[st], s * 64, key0, kv_bh, pol_kv);
+              tma_load_3d(sv + s * L::kSubBytes, &tm_v, &kv_full[st], s * 64, key0, kv_bh, pol_kv);
             }
           }
         }
@@ -284,12 +324,47 @@ __global__ void __launch_bounds__(384, 1)
           umma_commit_warp(&o_done[t]);
         };
         uint32_t kv_cnt = 0, it_cnt = 0, ep_cnt = 0, n_done = 0;
+        [[maybe_unused]] uint32_t pv_cnt = 0;
         bool ok = true;
         for (int rnd = 0, item = snake_item(0); ok && item < n_items; item = snake_item(++rnd), ++n_done) {
-          const FwdItem w = fwd_item(p, item);
+          const FwdItem w = get_item(item);
           const int nt = fwd_tile_of<D>(t, rnd) ? w.n1 : w.n0;   // key tiles of this warpgroup's query tile
           qb = n_done % L::kQBufs;
           if (!(ok = wait(&q_full[qb], (n_done / L::kQBufs) & 1))) break;
+          if constexpr (kWin) {
+            // the same walk, with it_cnt counting the S tiles issued and pv_cnt
+            // the P_bar V tiles; S of the next key tile is issued if it is taken
+            const int qt = fwd_tile_of<D>(t, rnd);
+            const uint32_t pv0 = pv_cnt;
+            auto next_s = [&](int j) {
+              if (!wait(&kv_full[(kv_cnt + j) % L::kStages], ((kv_cnt + j) / L::kStages) & 1)) return false;
+              if (it_cnt > 0 && !wait(&s_free[t], (it_cnt - 1) & 1)) return false;
+              tc_fence_after();
+              issue_s((kv_cnt + j) % L::kStages);
+              ++it_cnt;
+              if (j + 1 == nt) umma_commit_warp(&q_empty[qb]);   // a query tile's last key tile is never skipped
+              return true;
+            };
+            if (nt == 0) umma_commit_warp(&q_empty[qb]);
+            if (takes(w, qt, 0)) ok = next_s(0);
+            for (int j = 0; ok && j < w.nmax; ++j) {
+              const uint32_t st = (kv_cnt + j) % L::kStages;
+              if (takes(w, qt, j + 1) && !(ok = next_s(j + 1))) break;
+              if (takes(w, qt, j)) {
+                if (!(ok = wait(&p_full[t], pv_cnt & 1))) break;
+                if (pv_cnt == pv0 && !(ok = wait(&o_free[t], (ep_cnt & 1) ^ 1))) break;
+                tc_fence_after();
+                issue_pv(st, int(pv_cnt - pv0));
+                ++pv_cnt;
+              } else if (!(ok = wait(&kv_full[st], ((kv_cnt + j) / L::kStages) & 1))) {
+                break;
+              }
+              umma_commit_warp(&kv_empty[st]);
+            }
+            kv_cnt += w.nmax;
+            ep_cnt += (nt > 0) ? 1 : 0;
+            continue;
+          }
           if (nt > 0) {
             if (!(ok = wait(&kv_full[kv_cnt % L::kStages], (kv_cnt / L::kStages) & 1))) break;
             if (it_cnt > 0 && !(ok = wait(&s_free[t], (it_cnt - 1) & 1))) break;
@@ -369,12 +444,43 @@ __global__ void __launch_bounds__(384, 1)
         uint32_t n_done = 0;
         bool ok = true;
         for (int rnd = 0, item = snake_item(0); ok && item < n_items; item = snake_item(++rnd), ++n_done) {
-          const FwdItem w = fwd_item(p, item);
+          const FwdItem w = get_item(item);
           const int nt[2] = {w.n0, w.n1};
           if (!(ok = wait(q_full, n_done & 1) &&
                      wait(&kv_full[kv_cnt % L::kStages], (kv_cnt / L::kStages) & 1)))
             break;
           tc_fence_after();
+          if constexpr (kWin) {
+            // the same order, where a query tile leaves out the key tile that it
+            // does not see; it_cnt counts the P_bar V tiles issued
+            const uint32_t pv0[2] = {it_cnt[0], it_cnt[1]};
+            for (int t = 0; t < 2; ++t)
+              if (takes(w, t, 0)) issue_s(t, kv_cnt % L::kStages);
+            if (w.nmax == 1) umma_commit_warp(q_empty);
+            for (int j = 0; ok && j < w.nmax; ++j) {
+              const uint32_t st = (kv_cnt + j) % L::kStages;
+              const uint32_t nxt = kv_cnt + j + 1;
+              for (int t = 0; t < 2; ++t) {
+                if (takes(w, t, j)) {
+                  if (!(ok = wait(&p_full[t], it_cnt[t] & 1))) break;
+                  if (it_cnt[t] == pv0[t] && !(ok = wait(&o_free[t], (ep_cnt[t] & 1) ^ 1))) break;
+                  tc_fence_after();
+                  issue_pv(t, st, int(it_cnt[t] - pv0[t]));
+                  ++it_cnt[t];
+                }
+                if (t == 0 && j + 1 < w.nmax) {
+                  if (!(ok = wait(&kv_full[nxt % L::kStages], (nxt / L::kStages) & 1))) break;
+                  tc_fence_after();
+                }
+                if (t == 1) umma_commit_warp(&kv_empty[st]);
+                if (takes(w, t, j + 1)) issue_s(t, nxt % L::kStages);
+                if (t == 1 && j + 2 == w.nmax) umma_commit_warp(q_empty);
+              }
+            }
+            kv_cnt += w.nmax;
+            for (int t = 0; t < 2; ++t) ep_cnt[t] += (nt[t] > 0) ? 1 : 0;
+            continue;
+          }
           for (int t = 0; t < 2; ++t)
             if (nt[t] > 0) issue_s(t, kv_cnt % L::kStages);
           if (w.nmax == 1) umma_commit_warp(q_empty);
@@ -434,10 +540,11 @@ __global__ void __launch_bounds__(384, 1)
     bool ok = true;
 
     for (int rnd = 0, item = snake_item(0); ok && item < n_items; item = snake_item(++rnd)) {
-      const FwdItem w = fwd_item(p, item);
+      const FwdItem w = get_item(item);
       const int qt = fwd_tile_of<D>(t, rnd);   // which of the item's two query tiles
-      const int n_t = qt ? w.n1 : w.n0;
-      if (n_t == 0) continue;
+      const int skip = (kWin && qt) ? w.skip1 : -1;
+      const int n_t = (qt ? w.n1 : w.n0) - (skip >= 0 ? 1 : 0);   // key tiles taken
+      if (n_t <= 0) continue;
       const int row = w.q0_row + qt * 128 + (warp & 3) * 32 + lane;
       const int limit = p.causal ? min(row, p.N - 1) : p.N - 1;   // last visible key
 
@@ -470,11 +577,19 @@ __global__ void __launch_bounds__(384, 1)
 #pragma unroll
         for (int i = 0; i < 128; ++i) s[i] = __uint_as_float(r[i >> 5][i & 31]);
 
-        const int key0 = j * 128;
+        const int key0 = (kWin ? fwd_key_tile(w, j + (skip >= 0 && j >= skip ? 1 : 0)) : j) * 128;
         const bool masked = key0 + 127 > limit;
         if (masked) {
 #pragma unroll
           for (int i = 0; i < 128; ++i) s[i] = (key0 + i > limit) ? kNegInf : s[i];
+        }
+        if constexpr (kWin) {
+          // keys before the window that are no sinks: numbers a .. b - 1 of the tile
+          const int a = max(0, p.sinks - key0), b = row - p.window + 1 - key0;
+          if (a < b && a < 128) {
+#pragma unroll
+            for (int i = 0; i < 128; ++i) s[i] = (i >= a && i < b) ? kNegInf : s[i];
+          }
         }
         // tile maximum: eight 16-wide 3-input max chains, then a short tree
         float mx[8];
@@ -557,6 +672,7 @@ __global__ void __launch_bounds__(384, 1)
         if (raise && !raise_early) rs *= kFixFactor;
         // rescale of the running O and l: exact, whenever the shift moves
         float alpha = ex2(ms - ms_new);
+        if (kWin && m == kNegInf) alpha = 0.f;   // nothing seen so far: ms is no shift, and O and l are 0
         if (raise != raised) alpha = raise ? alpha * kFixFactor : alpha / kFixFactor;
         l = l * alpha + rs;
         if (j > 0) {

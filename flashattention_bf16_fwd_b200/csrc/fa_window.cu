@@ -1,0 +1,230 @@
+// fa_window.cu - the C ABI declared in include/fa_b200_window.h: argument
+// checks, tensor maps and launches of the windowed forward and backward.
+#include <cstdint>
+#include <mutex>
+
+#include "../../include/fa_b200_window.h"
+#include "fa_bwd.cuh"
+#include "fa_fwd.cuh"
+#include "fa_host.h"
+
+namespace fa {
+namespace {
+
+constexpr int kMaxDevices = 64;
+
+struct Setup {
+  std::once_flag once;
+  int status = FA_ERR_DEVICE;
+};
+Setup g_setup[kMaxDevices];
+
+// Large shared memory and the register count at launch that the kernels'
+// register split assumes, once per device.
+int setup_device() {
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDevices) return FA_ERR_DEVICE;
+  Setup* st = &g_setup[dev];
+  std::call_once(st->once, [st] {
+    bool ok = true, regs_ok = true;
+    auto setup = [&](auto kernel, int smem, int regs) {
+      cudaFuncAttributes a{};
+      ok &= cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) == cudaSuccess;
+      ok &= cudaFuncGetAttributes(&a, kernel) == cudaSuccess;
+      regs_ok &= a.numRegs == regs;
+    };
+    auto both = [&](auto elem) {
+      using E = decltype(elem);
+      setup(fa_fwd_kernel<64, false, E, true>, FwdLayout<64>::kAlloc, FwdLayout<64>::kLaunchRegs);
+      setup(fa_fwd_kernel<64, true, E, true>, FwdLayout<64>::kAlloc, FwdLayout<64>::kLaunchRegs);
+      setup(fa_fwd_kernel<128, false, E, true>, FwdLayout<128>::kAlloc, FwdLayout<128>::kLaunchRegs);
+      setup(fa_fwd_kernel<128, true, E, true>, FwdLayout<128>::kAlloc, FwdLayout<128>::kLaunchRegs);
+      setup(fa_bwd_kernel<64, E, false, true>, BwdLayout<64>::kAlloc, BwdLayout<64>::kLaunchRegs);
+      setup(fa_bwd_kernel<128, E, false, true>, BwdLayout<128>::kAlloc, BwdLayout<128>::kLaunchRegs);
+    };
+    both(ElemBF16{});
+    both(ElemF16{});
+    st->status = !ok ? FA_ERR_DEVICE : !regs_ok ? FA_ERR_BUILD : FA_OK;
+  });
+  return st->status;
+}
+
+int check_window(int B, int H, int Hkv, int N, int d, int window, int sinks, float scale) {
+  int rc = check_common(B, H, N, d, 1, scale);
+  if (rc != FA_OK) return rc;
+  if ((rc = check_heads(H, Hkv)) != FA_OK) return rc;
+  return window >= 1 && sinks >= 0 ? FA_OK : FA_ERR_WINDOW;
+}
+
+// How the backward divides the key tiles (BwdWindow), and where its workspace
+// keeps what.
+struct BwdPlan {
+  int window, sinks, near, split, chunks, chunk, part_rows;
+  size_t dsum, part, bytes;   // offsets; the dQ accumulator is at 0
+};
+
+BwdPlan bwd_plan(int B, int H, int Hkv, int N, int d, int window, int sinks) {
+  BwdPlan w{};
+  w.window = window < N ? window : N;
+  w.sinks = sinks < N ? sinks : N;
+  const int n_q = (N + 127) / 128;
+  w.near = (126 + w.window) / 128 + 1;
+  if (w.near > n_q) w.near = n_q;
+  const int far = n_q - w.near, sink_tiles = (w.sinks + 127) / 128;
+  w.split = sink_tiles < far ? sink_tiles : far;
+  // as many steps as a window has, and enough that K, V and the pieces are worth
+  // their loads; at least one per sink tile, so that no piece is empty
+  w.chunk = w.near > 8 ? w.near : 8;
+  if (w.chunk < sink_tiles) w.chunk = sink_tiles;
+  w.chunks = w.split ? (far + w.chunk - 1) / w.chunk : 0;
+  w.part_rows = w.sinks < 128 * w.split ? w.sinks : 128 * w.split;
+  const size_t rows = size_t(B) * H * N;
+  w.dsum = align256(rows * d * sizeof(float));
+  w.part = w.dsum + align256(rows * sizeof(float));
+  w.bytes = w.part + (w.split ? align256(size_t(B) * Hkv * (1 + w.chunks) * w.part_rows * 2 * d * sizeof(float)) : 0);
+  return w;
+}
+
+template <int D, typename E>
+int window_fwd(const void* q, const void* k, const void* v, void* o, float* lse, int B, int H, int Hkv, int N,
+               int window, int sinks, float scale, int fix_mode, int num_sms, int* dev_error, cudaStream_t stream) {
+  using L = FwdLayout<D>;
+  constexpr CUtensorMapDataType dt = map_type<E>();
+  CUtensorMap mq, mk, mv, mo;
+  if (!make_map(&mq, q, B * H, N, D, dt) || !make_map(&mk, k, B * Hkv, N, D, dt) ||
+      !make_map(&mv, v, B * Hkv, N, D, dt) || !make_map(&mo, o, B * H, N, D, dt, 32))
+    return FA_ERR_DEVICE;
+  FwdParams p{};
+  p.o = o;
+  p.lse = lse;
+  p.dev_error = dev_error;
+  p.BH = B * H;
+  p.N = N;
+  p.n_pairs = (N + 255) / 256;
+  p.causal = 1;
+  p.H = H;
+  p.group = H / Hkv;
+  p.scale_log2 = float(double(scale) * 1.4426950408889634);
+  set_fix(p, fix_mode, E::kMmaFmt == 0);
+  p.window = window < N ? window : N;
+  p.sinks = sinks < N ? sinks : N;
+  const int n_items = p.n_pairs * p.BH;
+  auto kern = fix_mode >= 4 ? fa_fwd_kernel<D, true, E, true> : fa_fwd_kernel<D, false, E, true>;
+  return launch(kern, dim3(n_items < num_sms ? n_items : num_sms), dim3(L::kThreads), L::kAlloc, stream, mq, mk, mv,
+                mo, p) == cudaSuccess
+             ? FA_OK
+             : FA_ERR_LAUNCH;
+}
+
+template <int D, typename E>
+int window_bwd(const void* q, const void* k, const void* v, const void* o, const float* lse, const void* dout,
+               void* dq, void* dk, void* dv, uint8_t* workspace, const BwdPlan& w, int B, int H, int Hkv, int N,
+               float scale, int num_sms, int* dev_error, cudaStream_t stream) {
+  using L = BwdLayout<D>;
+  using T = typename E::T;
+  constexpr CUtensorMapDataType dt = map_type<E>();
+  const int BH = B * H, BHkv = B * Hkv;
+  CUtensorMap mq, mk, mv, mdo, mdq, mdk, mdv;
+  if (!make_map(&mq, q, BH, N, D, dt) || !make_map(&mk, k, BHkv, N, D, dt) || !make_map(&mv, v, BHkv, N, D, dt) ||
+      !make_map(&mdo, dout, BH, N, D, dt) || !make_map_dq(&mdq, workspace, BH, N, D) ||
+      !make_map(&mdk, dk, BHkv, N, D, dt, 32) || !make_map(&mdv, dv, BHkv, N, D, dt, 32))
+    return FA_ERR_DEVICE;
+  float* dq_acc = reinterpret_cast<float*>(workspace);
+  float* dsum = reinterpret_cast<float*>(workspace + w.dsum);
+  float* part = reinterpret_cast<float*>(workspace + w.part);
+  const long long rows = (long long)BH * N;
+  if (launch(fa_bwd_pre_kernel<E>, dim3(unsigned((rows * 8 + 255) / 256)), dim3(256), 0, stream,
+             static_cast<const T*>(o), static_cast<const T*>(dout), dsum, dq_acc, rows, D) != cudaSuccess)
+    return FA_ERR_LAUNCH;
+  BwdParams p{};
+  p.lse = lse;
+  p.dsum = dsum;
+  p.dq_acc = dq_acc;
+  p.dk = dk;
+  p.dv = dv;
+  p.dev_error = dev_error;
+  p.BH = BHkv;
+  p.H = H;
+  p.group = H / Hkv;
+  p.N = N;
+  p.n_kv = (N + 127) / 128;
+  p.causal = 1;
+  p.scale = scale;
+  p.scale_log2 = float(double(scale) * 1.4426950408889634);
+  p.after_pre = 1;
+  p.window = w.window;
+  p.sinks = w.sinks;
+  p.near = w.near;
+  p.split = w.split;
+  p.chunks = w.chunks;
+  p.chunk = w.chunk;
+  p.part = part;
+  p.part_rows = w.part_rows;
+  const long long n_items = (long long)BHkv * (p.n_kv + w.split * w.chunks);
+  if (launch(fa_bwd_kernel<D, E, false, true>, dim3(unsigned(n_items < num_sms ? n_items : num_sms)),
+             dim3(L::kThreads), L::kAlloc, stream, mq, mk, mv, mdo, mdq, mdk, mdv, p) != cudaSuccess)
+    return FA_ERR_LAUNCH;
+  const long long n8 = rows * D / 8;
+  const unsigned dq_blocks = unsigned((n8 + 255) / 256);
+  const long long part_items = w.split ? (long long)BHkv * w.part_rows * (D / 2) : 0;
+  if (launch(fa_bwd_window_finish_kernel<E>, dim3(dq_blocks + unsigned((part_items + 255) / 256)), dim3(256), 0,
+             stream, static_cast<const float*>(dq_acc), static_cast<T*>(dq), scale, n8, dq_blocks,
+             static_cast<const float*>(part), static_cast<T*>(dk), static_cast<T*>(dv), 1 + w.chunks, w.part_rows, N,
+             D, part_items) != cudaSuccess)
+    return FA_ERR_LAUNCH;
+  return FA_OK;
+}
+
+}  // namespace
+}  // namespace fa
+
+using namespace fa;
+
+extern "C" {
+
+int fa_window_fwd(const void* q, const void* k, const void* v, void* o, float* lse, int B, int H, int Hkv, int N,
+                  int d, int window, int sinks, float scale, int fix_mode, int elem, void* stream) {
+  if (!q || !k || !v || !o || !lse) return FA_ERR_NULL;
+  int rc = check_window(B, H, Hkv, N, d, window, sinks, scale);
+  if (rc != FA_OK) return rc;
+  if (!aligned16(q) || !aligned16(k) || !aligned16(v) || !aligned16(o)) return FA_ERR_ALIGN;
+  if (fix_mode < 0 || fix_mode > 5) return FA_ERR_FIXMODE;
+  if (elem != FA_ELEM_BF16 && elem != FA_ELEM_F16) return FA_ERR_ARG;
+  int num_sms = 0, *dev_error = nullptr;
+  if ((rc = host_device(&num_sms, &dev_error)) != FA_OK || (rc = setup_device()) != FA_OK) return rc;
+  auto run = [&](auto fn) {
+    return fn(q, k, v, o, lse, B, H, Hkv, N, window, sinks, scale, fix_mode, num_sms, dev_error,
+              static_cast<cudaStream_t>(stream));
+  };
+  if (elem == FA_ELEM_BF16) return run(d == 64 ? window_fwd<64, ElemBF16> : window_fwd<128, ElemBF16>);
+  return run(d == 64 ? window_fwd<64, ElemF16> : window_fwd<128, ElemF16>);
+}
+
+size_t fa_window_bwd_workspace_size(int B, int H, int Hkv, int N, int d, int window, int sinks) {
+  if (check_window(B, H, Hkv, N, d, window, sinks, 1.f) != FA_OK) return 0;
+  return bwd_plan(B, H, Hkv, N, d, window, sinks).bytes;
+}
+
+int fa_window_bwd(const void* q, const void* k, const void* v, const void* o, const float* lse, const void* dout,
+                  void* dq, void* dk, void* dv, void* workspace, size_t workspace_bytes, int B, int H, int Hkv, int N,
+                  int d, int window, int sinks, float scale, int elem, void* stream) {
+  if (!q || !k || !v || !o || !lse || !dout || !dq || !dk || !dv) return FA_ERR_NULL;
+  int rc = check_window(B, H, Hkv, N, d, window, sinks, scale);
+  if (rc != FA_OK) return rc;
+  if (!aligned16(q) || !aligned16(k) || !aligned16(v) || !aligned16(o) || !aligned16(dout) || !aligned16(dq) ||
+      !aligned16(dk) || !aligned16(dv))
+    return FA_ERR_ALIGN;
+  if (elem != FA_ELEM_BF16 && elem != FA_ELEM_F16) return FA_ERR_ARG;
+  const BwdPlan w = bwd_plan(B, H, Hkv, N, d, window, sinks);
+  if (!workspace || !aligned16(workspace) || workspace_bytes < w.bytes) return FA_ERR_WORKSPACE;
+  int num_sms = 0, *dev_error = nullptr;
+  if ((rc = host_device(&num_sms, &dev_error)) != FA_OK || (rc = setup_device()) != FA_OK) return rc;
+  auto run = [&](auto fn) {
+    return fn(q, k, v, o, lse, dout, dq, dk, dv, static_cast<uint8_t*>(workspace), w, B, H, Hkv, N, scale, num_sms,
+              dev_error, static_cast<cudaStream_t>(stream));
+  };
+  if (elem == FA_ELEM_BF16) return run(d == 64 ? window_bwd<64, ElemBF16> : window_bwd<128, ElemBF16>);
+  return run(d == 64 ? window_bwd<64, ElemF16> : window_bwd<128, ElemF16>);
+}
+
+}  // extern "C"
