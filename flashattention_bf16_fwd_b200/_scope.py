@@ -1,33 +1,33 @@
-"""Device, stream and argument checks that the bindings of the window and cache calls share."""
-from __future__ import annotations
+"""Devices, streams and argument checks that the bindings of the window and cache calls share.
 
-import contextlib
+A call of this library takes some microseconds on the GPU for a single short
+sequence, so the bindings test everything in one expression and go through the
+checks below one by one only to say what is wrong.
+"""
+from __future__ import annotations
 
 import torch
 
-_HERE = contextlib.nullcontext()
 
-
-def scope(t, stream):
-    """The context in which a call on tensor ``t`` allocates and launches: t's
-    device is current, and ``stream`` (a torch stream or a cudaStream_t; None:
-    the device's current stream) is the current stream, so that what the call
-    allocates belongs to the stream that uses it."""
-    if not t.is_cuda:
+def call(fn, t, stream, *args):
+    """fn(*args, stream) with t's device current and ``stream`` (a torch stream or
+    a cudaStream_t; None: the device's current stream) the current stream, so
+    that what fn allocates belongs to the stream that uses it."""
+    at = t.get_device()
+    if at < 0:
         raise ValueError("tensors must live on a CUDA device (the library has no CPU path)")
     if stream is None:
-        return _HERE if t.get_device() == torch.cuda.current_device() else torch.cuda.device(t.device)
+        if at == torch.cuda.current_device():
+            return fn(*args, torch._C._cuda_getCurrentRawStream(at))
+        with torch.cuda.device(at):
+            return fn(*args, torch._C._cuda_getCurrentRawStream(at))
     if not isinstance(stream, torch.cuda.Stream):
         stream = (torch.cuda.ExternalStream(int(stream), device=t.device) if int(stream)
                   else torch.cuda.default_stream(t.device))
     if stream.device != t.device:
         raise ValueError(f"the stream is on {stream.device}, the tensors on {t.device}")
-    return torch.cuda.stream(stream)
-
-
-def current() -> int:
-    """The current device's current stream."""
-    return torch.cuda.current_stream().cuda_stream
+    with torch.cuda.stream(stream):
+        return fn(*args, stream.cuda_stream)
 
 
 def same_device(t, *others):

@@ -8,11 +8,12 @@ fewer, every fix_mode.
 from __future__ import annotations
 
 import ctypes
+import functools
 
 import torch
 
 from . import _scope
-from .fa import _check, _elem, _shape, _validate, lib
+from .fa import _check, _elem, _validate, lib
 
 __all__ = ["EXPORTED", "fa_window_bwd_workspace_size", "attention_window_fwd", "attention_window_bwd"]
 
@@ -25,22 +26,37 @@ lib.fa_window_bwd_workspace_size.restype = _sz
 lib.fa_window_bwd.argtypes = [_vp] * 10 + [_sz] + [_i] * 7 + [_f, _i, _vp]
 
 
+@functools.lru_cache(maxsize=256)
 def fa_window_bwd_workspace_size(B: int, H: int, Hkv: int, N: int, d: int, window: int, sinks: int) -> int:
     return int(lib.fa_window_bwd_workspace_size(B, H, Hkv, N, d, _scope.count(window), _scope.count(sinks)))
+
+
+def _valid(q, k, v) -> bool:
+    """What _validate asks of q, k and v, in one expression."""
+    shape, dtype, at = k.shape, q.dtype, q.get_device()
+    return bool(len(q.shape) == 4 == len(shape) and shape == v.shape and shape[0] == q.shape[0]
+                and shape[2:] == q.shape[2:] and shape[1] and q.shape[1] % shape[1] == 0 and dtype is k.dtype
+                and dtype is v.dtype and at == k.get_device() == v.get_device() and q.is_contiguous()
+                and k.is_contiguous() and v.is_contiguous())
 
 
 def attention_window_fwd(q, k, v, window: int, sinks: int = 0, scale: float | None = None, fix_mode: int = 1,
                          stream=None):
     """Allocate O and LSE and run the forward; returns (o, lse)."""
-    _validate(q, k, v)
-    B, H, N, d = _shape(q)
-    with _scope.scope(q, stream):
-        o = torch.empty_like(q)
-        lse = torch.empty((B, H, N), dtype=torch.float32, device=q.device)
-        _check("fa_window_fwd", lib.fa_window_fwd(
-            q.data_ptr(), k.data_ptr(), v.data_ptr(), o.data_ptr(), lse.data_ptr(), B, H, int(k.shape[1]), N, d,
-            _scope.count(window), _scope.count(sinks), d ** -0.5 if scale is None else float(scale), int(fix_mode),
-            _elem(q), _scope.current()))
+    if not _valid(q, k, v):
+        _validate(q, k, v)
+    return _scope.call(_fwd, q, stream, q, k, v, window, sinks, scale, fix_mode, _elem(q))
+
+
+def _fwd(q, k, v, window, sinks, scale, fix_mode, elem, stream):
+    B, H, N, d = q.shape
+    o = torch.empty_like(q)
+    lse = q.new_empty((B, H, N), dtype=torch.float32)
+    status = lib.fa_window_fwd(q.data_ptr(), k.data_ptr(), v.data_ptr(), o.data_ptr(), lse.data_ptr(), B, H, k.shape[1], N,
+                               d, _scope.count(window), _scope.count(sinks), d ** -0.5 if scale is None else scale,
+                               fix_mode, elem, stream)
+    if status:
+        _check("fa_window_fwd", status)
     return o, lse
 
 
@@ -48,20 +64,24 @@ def attention_window_bwd(q, k, v, o, lse, do, window: int, sinks: int = 0, scale
                          workspace=None):
     """Allocate dQ, dK, dV (and the workspace unless given) and run the
     backward of attention_window_fwd with the same window and sinks."""
-    _validate(q, k, v, (o, do))
-    B, H, N, d = _shape(q)
-    if lse.shape != (B, H, N) or lse.dtype != torch.float32 or not lse.is_contiguous():
+    if not (_valid(q, k, v) and o.shape == q.shape == do.shape and o.dtype is q.dtype is do.dtype
+            and o.get_device() == q.get_device() == do.get_device() and o.is_contiguous() and do.is_contiguous()):
+        _validate(q, k, v, (o, do))
+    if lse.shape != q.shape[:3] or lse.dtype != torch.float32 or not lse.is_contiguous():
         raise ValueError("lse must be a contiguous float32 [B, H, N] tensor")
     _scope.same_device(q, lse, workspace)
-    Hkv = int(k.shape[1])
-    with _scope.scope(q, stream):
-        dq, dk, dv = torch.empty_like(q), torch.empty_like(k), torch.empty_like(v)
-        if workspace is None:
-            workspace = torch.empty(fa_window_bwd_workspace_size(B, H, Hkv, N, d, window, sinks), dtype=torch.uint8,
-                                    device=q.device)
-        _check("fa_window_bwd", lib.fa_window_bwd(
-            q.data_ptr(), k.data_ptr(), v.data_ptr(), o.data_ptr(), lse.data_ptr(), do.data_ptr(), dq.data_ptr(),
-            dk.data_ptr(), dv.data_ptr(), workspace.data_ptr(), workspace.numel() * workspace.element_size(), B, H, Hkv,
-            N, d, _scope.count(window), _scope.count(sinks), d ** -0.5 if scale is None else float(scale), _elem(q),
-            _scope.current()))
+    return _scope.call(_bwd, q, stream, q, k, v, o, lse, do, window, sinks, scale, workspace, _elem(q))
+
+
+def _bwd(q, k, v, o, lse, do, window, sinks, scale, workspace, elem, stream):
+    B, H, N, d = q.shape
+    Hkv, window, sinks = k.shape[1], _scope.count(window), _scope.count(sinks)
+    dq, dk, dv = torch.empty_like(q), torch.empty_like(k), torch.empty_like(v)
+    if workspace is None:
+        workspace = q.new_empty(fa_window_bwd_workspace_size(B, H, Hkv, N, d, window, sinks), dtype=torch.uint8)
+    status = lib.fa_window_bwd(q.data_ptr(), k.data_ptr(), v.data_ptr(), o.data_ptr(), lse.data_ptr(), do.data_ptr(),
+                               dq.data_ptr(), dk.data_ptr(), dv.data_ptr(), workspace.data_ptr(), workspace.nbytes, B, H,
+                               Hkv, N, d, window, sinks, d ** -0.5 if scale is None else scale, elem, stream)
+    if status:
+        _check("fa_window_bwd", status)
     return dq, dk, dv
