@@ -64,6 +64,9 @@ struct FwdParams {
   int window, sinks;    // windowed kernel: key j is visible where j <= i and (i - j < window or j < sinks)
 };
 
+// A word whose n lowest bits are set (n <= 0: none, n >= 32: all).
+__device__ __forceinline__ uint32_t low_bits(int n) { return n <= 0 ? 0u : 0xffffffffu >> (32 - min(n, 32)); }
+
 template <int D>
 struct FwdLayout {
   static constexpr int kStages = (D == 64) ? 4 : 2;   // K/V ring depth
@@ -578,6 +581,110 @@ __global__ void __launch_bounds__(384, 1)
         for (int i = 0; i < 128; ++i) s[i] = __uint_as_float(r[i >> 5][i & 31]);
 
         const int key0 = (kWin ? fwd_key_tile(w, j + (skip >= 0 && j >= skip ? 1 : 0)) : j) * 128;
+        if constexpr (kWin && !kVariants) {
+          // Which keys a row sees, as bits, where the warp's rows do not see all.
+          const int row0 = row - lane;
+          if (key0 + 127 > min(row0, p.N - 1) || (key0 + 127 >= p.sinks && key0 < row0 + 32 - p.window)) {
+            const int hi = limit - key0, lo = row - p.window + 1 - key0, sk = p.sinks - key0;
+#pragma unroll
+            for (int c = 0; c < 4; ++c) {
+              const uint32_t see = low_bits(hi + 1 - 32 * c) & (~low_bits(lo - 32 * c) | low_bits(sk - 32 * c));
+#pragma unroll
+              for (int i = 0; i < 32; ++i) s[32 * c + i] = (see >> i & 1u) ? s[32 * c + i] : kNegInf;
+            }
+          }
+          // The tile's maximum, and whether it occurs twice: as an 8 x 16 grid,
+          // two entries differ in their row or their column, so that a repeated
+          // maximum is the maximum of two rows or of two columns.  That takes 24
+          // comparisons instead of 128, and is known before the exponentials,
+          // which then use the final shift.
+          float rmax[8], cmax[16];
+#pragma unroll
+          for (int g = 0; g < 8; ++g) {
+            float a = fmax3(s[16 * g], s[16 * g + 1], s[16 * g + 2]);
+#pragma unroll
+            for (int i = 3; i < 15; i += 2) a = fmax3(a, s[16 * g + i], s[16 * g + i + 1]);
+            rmax[g] = fmaxf(a, s[16 * g + 15]);
+          }
+#pragma unroll
+          for (int g = 0; g < 16; ++g)
+            cmax[g] = fmax3(fmax3(s[g], s[16 + g], s[32 + g]), fmax3(s[48 + g], s[64 + g], s[80 + g]),
+                            fmaxf(s[96 + g], s[112 + g]));
+          const float mt = fmax3(fmax3(rmax[0], rmax[1], rmax[2]), fmax3(rmax[3], rmax[4], rmax[5]),
+                                 fmaxf(rmax[6], rmax[7]));
+          float n_rows = 0.f, n_cols = 0.f;
+#pragma unroll
+          for (int g = 0; g < 8; ++g) n_rows += (rmax[g] == mt) ? 1.f : 0.f;
+#pragma unroll
+          for (int g = 0; g < 16; ++g) n_cols += (cmax[g] == mt) ? 1.f : 0.f;
+          const float m_new = fmaxf(m, mt);
+          const float ms_new = (m_new == kNegInf) ? 0.f : m_new * sl2;
+          // how often the running maximum has occurred: 0, 1, or 2 and more
+          int c_new = (m == m_new ? cnt : 0) + (mt == m_new ? (n_rows + n_cols > 2.f ? 2 : 1) : 0);
+          if (m_new == kNegInf) c_new = 0;
+          const bool raise = p.fix && c_new >= 2;
+          const float msh = raise ? ms_new + p.delta_log2 : ms_new;
+          float alpha = ex2(ms - ms_new);
+          if (raise != raised) alpha = raise ? alpha * kFixFactor : alpha / kFixFactor;
+          if (m == kNegInf) alpha = 0.f;           // nothing seen so far: ms is no shift, and O and l are 0
+          // P_bar V of the tile before must be finished: it read the P_bar buffer
+          // and O_t must hold its result before O_t is rescaled
+          if (j > 0) {
+            ok = __all_sync(0xffffffffu, mbar_wait(&o_done[t], (it_cnt + j - 1) & 1, wd));
+            if (!ok) break;
+            tc_fence_after();
+          }
+          const bool rescale = j > 0 && __any_sync(0xffffffffu, alpha != 1.f);
+          uint64_t sum2[4] = {0, 0, 0, 0};
+          const uint64_t sl2_2 = f2_pack(sl2, sl2), nmsh_2 = f2_pack(-msh, -msh), a2 = f2_pack(alpha, alpha);
+          // four times 32 keys; a quarter of O_t is rescaled beside each
+#pragma unroll
+          for (int c = 0; c < 4; ++c) {
+            uint32_t o[D / 4];
+            if (rescale) {
+              if constexpr (D == 128)
+                tmem_ld32(t_o + c * 32, o);
+              else
+                tmem_ld16(t_o + c * 16, o);
+            }
+            uint32_t pk[16];
+#pragma unroll
+            for (int i = 0; i < 16; ++i) {
+              float x0, x1;
+              f2_unpack(f2_fma(f2_pack(s[32 * c + 2 * i], s[32 * c + 2 * i + 1]), sl2_2, nmsh_2), x0, x1);
+              x0 = ex2(x0);
+              x1 = ex2(x1);
+              sum2[i & 3] = f2_add(sum2[i & 3], f2_pack(x0, x1));
+              pk[i] = E::pack(x0, x1);
+            }
+            tmem_st16(t_p + c * 16, pk);
+            if (rescale) {
+              tmem_ld_wait(o);
+#pragma unroll
+              for (int i = 0; i < D / 8; ++i) {
+                float y0, y1;
+                f2_unpack(f2_mul(f2_pack(__uint_as_float(o[2 * i]), __uint_as_float(o[2 * i + 1])), a2), y0, y1);
+                o[2 * i] = __float_as_uint(y0);
+                o[2 * i + 1] = __float_as_uint(y1);
+              }
+              if constexpr (D == 128)
+                tmem_st32(t_o + c * 32, o);
+              else
+                tmem_st16(t_o + c * 16, o);
+            }
+          }
+          float ea, eb;
+          f2_unpack(f2_add(f2_add(sum2[0], sum2[1]), f2_add(sum2[2], sum2[3])), ea, eb);
+          l = l * alpha + (ea + eb);
+          tmem_st_wait();
+          tc_fence_before();
+          mbar_arrive(&p_full[t]);
+          m = m_new;
+          cnt = c_new;
+          ms = ms_new;
+          raised = raise;
+          continue;
+        }
         const bool masked = key0 + 127 > limit;
         if (masked) {
 #pragma unroll
