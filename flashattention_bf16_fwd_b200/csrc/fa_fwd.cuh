@@ -169,7 +169,9 @@ __device__ __forceinline__ constexpr float rounds_to_one() {
 // before rounding); the other instantiation, used for fix_mode 0-3 without
 // records, leaves all of it out.
 // kWin: the windowed kernel, in which each query sees the keys of its window and
-// the sinks: the same pipeline over a shorter list of key tiles.
+// the sinks: the same pipeline over a shorter list of key tiles.  Without
+// kVariants it is fix_mode 1's, with a softmax of its own; the other fix_modes
+// take the kVariants instantiation, whose softmax is the one below.
 template <int D, bool kVariants, typename E = ElemBF16, bool kWin = false>
 __global__ void __launch_bounds__(384, 1)
     fa_fwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
@@ -582,107 +584,99 @@ __global__ void __launch_bounds__(384, 1)
 
         const int key0 = (kWin ? fwd_key_tile(w, j + (skip >= 0 && j >= skip ? 1 : 0)) : j) * 128;
         if constexpr (kWin && !kVariants) {
-          // Which keys a row sees, as bits, where the warp's rows do not see all.
-          const int row0 = row - lane;
-          if (key0 + 127 > min(row0, p.N - 1) || (key0 + 127 >= p.sinks && key0 < row0 + 32 - p.window)) {
-            const int hi = limit - key0, lo = row - p.window + 1 - key0, sk = p.sinks - key0;
+          // fix_mode 1 with a shift that stays above the running maximum.  The
+          // shift is set to the maximum + delta + kHeadroom and left there until
+          // the maximum + delta passes it, so that every exponential is below 1
+          // on every row, repeated maxima or not (a maximum maps to at most 1 -
+          // 2^-8, in fp16 1 - 2^-11).  The exact shift moves in most tiles for
+          // one of a warp's 32 rows, and each move rescales O_t through TMEM;
+          // with headroom that is rare after the first tile, and nothing counts
+          // repetitions.  P scaled by a power of two is rounded alike in bf16; in
+          // fp16 the headroom is smaller, for P below 2^-14 loses bits there.
+          // N = 16384, window 4096, d = 128: 1186 us with the exact shift,
+          // 936 us with headroom.
+          constexpr float kHeadroom = E::kMmaFmt == 1 ? 8.f : 4.f;
+          auto tile = [&](auto edge) {
+            if constexpr (decltype(edge)::value) {     // which keys each row sees, as bits
+              const int hi = limit - key0, lo = row - p.window + 1 - key0, sk = p.sinks - key0;
+#pragma unroll
+              for (int c = 0; c < 4; ++c) {
+                const uint32_t see = low_bits(hi + 1 - 32 * c) & (~low_bits(lo - 32 * c) | low_bits(sk - 32 * c));
+#pragma unroll
+                for (int i = 0; i < 32; ++i) s[32 * c + i] = (see >> i & 1u) ? s[32 * c + i] : kNegInf;
+              }
+            }
+            float mx[8];
+#pragma unroll
+            for (int g = 0; g < 8; ++g) {
+              float a = fmax3(s[16 * g], s[16 * g + 1], s[16 * g + 2]);
+#pragma unroll
+              for (int i = 3; i < 15; i += 2) a = fmax3(a, s[16 * g + i], s[16 * g + i + 1]);
+              mx[g] = fmaxf(a, s[16 * g + 15]);
+            }
+            const float top = fmaf(fmax3(fmax3(mx[0], mx[1], mx[2]), fmax3(mx[3], mx[4], mx[5]), fmaxf(mx[6], mx[7])),
+                                   sl2, p.delta_log2);
+            // ms: the shift in use; -inf where the row has seen nothing
+            float alpha = 1.f;
+            if (top > ms) {
+              const float shift = top + kHeadroom;
+              alpha = ex2(ms - shift);
+              ms = shift;
+            }
+            // P_bar V of the tile before must be finished: it read the P_bar buffer
+            // and O_t must hold its result before O_t is rescaled
+            if (j > 0) {
+              if (!__all_sync(0xffffffffu, mbar_wait(&o_done[t], (it_cnt + j - 1) & 1, wd))) return false;
+              tc_fence_after();
+            }
+            if (j > 0 && __any_sync(0xffffffffu, alpha != 1.f)) {
+              const uint64_t a2 = f2_pack(alpha, alpha);
+#pragma unroll 1
+              for (int c = 0; c < D / 32; ++c) {
+                uint32_t o[32];
+                tmem_ld32(t_o + c * 32, o);
+                tmem_ld_wait(o);
+#pragma unroll
+                for (int i = 0; i < 16; ++i) {
+                  float y0, y1;
+                  f2_unpack(f2_mul(f2_pack(__uint_as_float(o[2 * i]), __uint_as_float(o[2 * i + 1])), a2), y0, y1);
+                  o[2 * i] = __float_as_uint(y0);
+                  o[2 * i + 1] = __float_as_uint(y1);
+                }
+                tmem_st32(t_o + c * 32, o);
+              }
+            }
+            uint64_t sum2[4] = {0, 0, 0, 0};
+            const float nms = ms == kNegInf ? 0.f : -ms;
+            const uint64_t sl2_2 = f2_pack(sl2, sl2), nms_2 = f2_pack(nms, nms);
 #pragma unroll
             for (int c = 0; c < 4; ++c) {
-              const uint32_t see = low_bits(hi + 1 - 32 * c) & (~low_bits(lo - 32 * c) | low_bits(sk - 32 * c));
+              uint32_t pk[16];
 #pragma unroll
-              for (int i = 0; i < 32; ++i) s[32 * c + i] = (see >> i & 1u) ? s[32 * c + i] : kNegInf;
-            }
-          }
-          // The tile's maximum, and whether it occurs twice: as an 8 x 16 grid,
-          // two entries differ in their row or their column, so that a repeated
-          // maximum is the maximum of two rows or of two columns.  That takes 24
-          // comparisons instead of 128, and is known before the exponentials,
-          // which then use the final shift.
-          float rmax[8], cmax[16];
-#pragma unroll
-          for (int g = 0; g < 8; ++g) {
-            float a = fmax3(s[16 * g], s[16 * g + 1], s[16 * g + 2]);
-#pragma unroll
-            for (int i = 3; i < 15; i += 2) a = fmax3(a, s[16 * g + i], s[16 * g + i + 1]);
-            rmax[g] = fmaxf(a, s[16 * g + 15]);
-          }
-#pragma unroll
-          for (int g = 0; g < 16; ++g)
-            cmax[g] = fmax3(fmax3(s[g], s[16 + g], s[32 + g]), fmax3(s[48 + g], s[64 + g], s[80 + g]),
-                            fmaxf(s[96 + g], s[112 + g]));
-          const float mt = fmax3(fmax3(rmax[0], rmax[1], rmax[2]), fmax3(rmax[3], rmax[4], rmax[5]),
-                                 fmaxf(rmax[6], rmax[7]));
-          float n_rows = 0.f, n_cols = 0.f;
-#pragma unroll
-          for (int g = 0; g < 8; ++g) n_rows += (rmax[g] == mt) ? 1.f : 0.f;
-#pragma unroll
-          for (int g = 0; g < 16; ++g) n_cols += (cmax[g] == mt) ? 1.f : 0.f;
-          const float m_new = fmaxf(m, mt);
-          const float ms_new = (m_new == kNegInf) ? 0.f : m_new * sl2;
-          // how often the running maximum has occurred: 0, 1, or 2 and more
-          int c_new = (m == m_new ? cnt : 0) + (mt == m_new ? (n_rows + n_cols > 2.f ? 2 : 1) : 0);
-          if (m_new == kNegInf) c_new = 0;
-          const bool raise = p.fix && c_new >= 2;
-          const float msh = raise ? ms_new + p.delta_log2 : ms_new;
-          float alpha = ex2(ms - ms_new);
-          if (raise != raised) alpha = raise ? alpha * kFixFactor : alpha / kFixFactor;
-          if (m == kNegInf) alpha = 0.f;           // nothing seen so far: ms is no shift, and O and l are 0
-          // P_bar V of the tile before must be finished: it read the P_bar buffer
-          // and O_t must hold its result before O_t is rescaled
-          if (j > 0) {
-            ok = __all_sync(0xffffffffu, mbar_wait(&o_done[t], (it_cnt + j - 1) & 1, wd));
-            if (!ok) break;
-            tc_fence_after();
-          }
-          const bool rescale = j > 0 && __any_sync(0xffffffffu, alpha != 1.f);
-          uint64_t sum2[4] = {0, 0, 0, 0};
-          const uint64_t sl2_2 = f2_pack(sl2, sl2), nmsh_2 = f2_pack(-msh, -msh), a2 = f2_pack(alpha, alpha);
-          // four times 32 keys; a quarter of O_t is rescaled beside each
-#pragma unroll
-          for (int c = 0; c < 4; ++c) {
-            uint32_t o[D / 4];
-            if (rescale) {
-              if constexpr (D == 128)
-                tmem_ld32(t_o + c * 32, o);
-              else
-                tmem_ld16(t_o + c * 16, o);
-            }
-            uint32_t pk[16];
-#pragma unroll
-            for (int i = 0; i < 16; ++i) {
-              float x0, x1;
-              f2_unpack(f2_fma(f2_pack(s[32 * c + 2 * i], s[32 * c + 2 * i + 1]), sl2_2, nmsh_2), x0, x1);
-              x0 = ex2(x0);
-              x1 = ex2(x1);
-              sum2[i & 3] = f2_add(sum2[i & 3], f2_pack(x0, x1));
-              pk[i] = E::pack(x0, x1);
-            }
-            tmem_st16(t_p + c * 16, pk);
-            if (rescale) {
-              tmem_ld_wait(o);
-#pragma unroll
-              for (int i = 0; i < D / 8; ++i) {
-                float y0, y1;
-                f2_unpack(f2_mul(f2_pack(__uint_as_float(o[2 * i]), __uint_as_float(o[2 * i + 1])), a2), y0, y1);
-                o[2 * i] = __float_as_uint(y0);
-                o[2 * i + 1] = __float_as_uint(y1);
+              for (int i = 0; i < 16; ++i) {
+                float x0, x1;
+                f2_unpack(f2_fma(f2_pack(s[32 * c + 2 * i], s[32 * c + 2 * i + 1]), sl2_2, nms_2), x0, x1);
+                x0 = ex2(x0);
+                x1 = ex2(x1);
+                sum2[i & 3] = f2_add(sum2[i & 3], f2_pack(x0, x1));
+                pk[i] = E::pack(x0, x1);
               }
-              if constexpr (D == 128)
-                tmem_st32(t_o + c * 32, o);
-              else
-                tmem_st16(t_o + c * 16, o);
+              tmem_st16(t_p + c * 16, pk);
             }
-          }
-          float ea, eb;
-          f2_unpack(f2_add(f2_add(sum2[0], sum2[1]), f2_add(sum2[2], sum2[3])), ea, eb);
-          l = l * alpha + (ea + eb);
+            float ea, eb;
+            f2_unpack(f2_add(f2_add(sum2[0], sum2[1]), f2_add(sum2[2], sum2[3])), ea, eb);
+            l = l * alpha + (ea + eb);
+            return true;
+          };
+          const int row0 = row - lane;                 // the warp's first row
+          if (key0 + 127 > min(row0, p.N - 1) || (key0 + 127 >= p.sinks && key0 < row0 + 32 - p.window))
+            ok = tile(std::true_type{});
+          else
+            ok = tile(std::false_type{});
+          if (!ok) break;
           tmem_st_wait();
           tc_fence_before();
           mbar_arrive(&p_full[t]);
-          m = m_new;
-          cnt = c_new;
-          ms = ms_new;
-          raised = raise;
           continue;
         }
         const bool masked = key0 + 127 > limit;

@@ -109,7 +109,7 @@ int window_fwd(const void* q, const void* k, const void* v, void* o, float* lse,
   p.window = window < N ? window : N;
   p.sinks = sinks < N ? sinks : N;
   const int n_items = p.n_pairs * p.BH;
-  auto kern = fix_mode >= 4 ? fa_fwd_kernel<D, true, E, true> : fa_fwd_kernel<D, false, E, true>;
+  auto kern = fix_mode == 1 ? fa_fwd_kernel<D, false, E, true> : fa_fwd_kernel<D, true, E, true>;
   return launch(kern, dim3(n_items < num_sms ? n_items : num_sms), dim3(L::kThreads), L::kAlloc, stream, mq, mk, mv,
                 mo, p) == cudaSuccess
              ? FA_OK

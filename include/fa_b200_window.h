@@ -26,6 +26,11 @@ extern "C" {
 /*
  * fa_window_fwd - forward pass: fa_fwd_ex with the mask above.
  *   q, o : [B,H,N,d];  k, v : [B,Hkv,N,d], Hkv dividing H;  lse : float32 [B,H,N].
+ *   fix_mode : 0, 2, 3, 4, 5 as in fa_fwd.  1, the fast one, applies the fix to
+ *       every row: the shift stays above the running maximum, by 2^8 at most (in
+ *       fp16 2^4), so that every exponential, the maxima included, is below 1
+ *       whether or not the maximum is repeated; a maximum maps to 1 - 2^-8 (fp16
+ *       1 - 2^-11) times a power of two where it set the shift.
  */
 FA_API int fa_window_fwd(const void* q, const void* k, const void* v, void* o, float* lse, int B, int H, int Hkv,
                          int N, int d, int window, int sinks, float scale, int fix_mode, int elem, void* stream);

@@ -8,8 +8,9 @@ move it, from the arithmetic (h = half a step of the element format, eps / 2):
   (reach_i = scale max_j sum |q_i||k_j|), its exponential by that and by
   2^-22 (4 + 2 reach_i) for the exponent's rounding and ex2: e_i together;
 * P_bar is rounded to the element format before P_bar V: h of each P, and in
-  fp16 2^-25 absolute where P is below 2^-14 (subnormals; twice that, for the
-  row sum is at least 1/2 under any shift of the fix);
+  fp16 2^-25 absolute where P is below 2^-14 (subnormals).  The shift is at most
+  2^4 times 1 / (1 - 2^-11) above the maximum in fp16 (fix_mode 1), or maps it to
+  1/2 (fix_mode 2), so that this is at most 2^5 times 2^-25 of the maximum's P;
 * O is rounded: h |O|, or in fp16 2^-25 where |O| is below 2^-14 (half a
   subnormal step), and so is each gradient;
 * in the backward, P = exp(S - LSE) is off by 2 e_i (LSE carries e_i too) and is
@@ -48,7 +49,7 @@ def _forward(q, k, v, scale, vis, h, sub):
     p = e / l
     o, lse = p @ v, (m + np.log(l))[:, 0]
     err = _row_errors(q, k, scale, vis)
-    tol = np.maximum(h * np.abs(o), sub) + (h * (1 + 2 * h) + 2 * err + 2.0 ** -18) * (p @ np.abs(v)) + 2 * sub * (vis @ np.abs(v)) / l
+    tol = np.maximum(h * np.abs(o), sub) + (h * (1 + 2 * h) + 2 * err + 2.0 ** -18) * (p @ np.abs(v)) + 32 * sub * (vis @ np.abs(v)) / l
     return p, o, lse, tol, err
 
 

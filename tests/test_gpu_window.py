@@ -93,12 +93,24 @@ def test_fix_modes_on_repeated_maxima(fa, fix, d, dt):
 
 
 def test_window_as_wide_as_the_sequence_is_causal_attention(fa):
-    """The same tiles in the same order: the forward's bits are those of attention_fwd."""
+    """The same tiles in the same order: the bits are those of attention_fwd in the modes that share its softmax."""
     for d, N in ((64, 900), (128, 777)):
         x = [t.cuda() for t in draw(1, 4, 2, N, d, "bf16", 3)]
-        o, lse = fa.window.attention_window_fwd(*x[:3], N, 0)
-        o2, lse2 = fa.attention_fwd(*x[:3], causal=True)
-        assert torch.equal(o, o2) and torch.equal(lse, lse2)
+        for fix in (0, 2, 3, 4, 5):
+            o, lse = fa.window.attention_window_fwd(*x[:3], N, 0, fix_mode=fix)
+            o2, lse2 = fa.attention_fwd(*x[:3], causal=True, fix_mode=fix)
+            assert torch.equal(o, o2) and torch.equal(lse, lse2), fix
+
+
+@pytest.mark.parametrize("d,dt", [(64, "bf16"), (128, "bf16"), (64, "fp16"), (128, "fp16")])
+def test_rising_and_falling_scores(fa, d, dt):
+    """Scores that rise by more than the shift's headroom from tile to tile, or fall by thousands: every key tile
+    moves the shift, or none after the first does and P underflows."""
+    for sign in (1, -1):
+        x = draw(1, 2, 2, 900, d, dt, 12)
+        x[0][..., 0] = 16
+        x[1][..., 0] = torch.linspace(-20, 20, 900) * sign
+        check(fa, x, 500, 130, scale=0.5, bwd=False)
 
 
 def test_many_items_and_repeats(fa):
