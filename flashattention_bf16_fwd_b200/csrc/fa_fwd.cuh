@@ -597,22 +597,33 @@ __global__ void __launch_bounds__(384, 1)
           // 936 us with headroom.
           constexpr float kHeadroom = E::kMmaFmt == 1 ? 8.f : 4.f;
           auto tile = [&](auto edge) {
-            if constexpr (decltype(edge)::value) {     // which keys each row sees, as bits
-              const int hi = limit - key0, lo = row - p.window + 1 - key0, sk = p.sinks - key0;
-#pragma unroll
-              for (int c = 0; c < 4; ++c) {
-                const uint32_t see = low_bits(hi + 1 - 32 * c) & (~low_bits(lo - 32 * c) | low_bits(sk - 32 * c));
-#pragma unroll
-                for (int i = 0; i < 32; ++i) s[32 * c + i] = (see >> i & 1u) ? s[32 * c + i] : kNegInf;
-              }
-            }
+            // A tile in which some row of the warp does not see every key is taken
+            // 32 keys at a time: which of them each row sees, as bits; a piece
+            // that no row sees is left out (of a sink tile all but the sinks', of
+            // a diagonal tile those above the warp's rows).
+            constexpr bool kEdge = decltype(edge)::value;
+            bool any[4] = {true, true, true, true};
             float mx[8];
 #pragma unroll
-            for (int g = 0; g < 8; ++g) {
-              float a = fmax3(s[16 * g], s[16 * g + 1], s[16 * g + 2]);
+            for (int c = 0; c < 4; ++c) {
+              mx[2 * c] = mx[2 * c + 1] = kNegInf;
+              if constexpr (kEdge) {
+                const int hi = limit - key0, lo = row - p.window + 1 - key0, sk = p.sinks - key0;
+                const uint32_t see = low_bits(hi + 1 - 32 * c) & (~low_bits(lo - 32 * c) | low_bits(sk - 32 * c));
+                any[c] = __any_sync(0xffffffffu, see != 0u);
+                if (any[c] && __any_sync(0xffffffffu, see != 0xffffffffu)) {
 #pragma unroll
-              for (int i = 3; i < 15; i += 2) a = fmax3(a, s[16 * g + i], s[16 * g + i + 1]);
-              mx[g] = fmaxf(a, s[16 * g + 15]);
+                  for (int i = 0; i < 32; ++i) s[32 * c + i] = (see >> i & 1u) ? s[32 * c + i] : kNegInf;
+                }
+              }
+              if (!any[c]) continue;
+#pragma unroll
+              for (int g = 2 * c; g < 2 * c + 2; ++g) {
+                float a = fmax3(s[16 * g], s[16 * g + 1], s[16 * g + 2]);
+#pragma unroll
+                for (int i = 3; i < 15; i += 2) a = fmax3(a, s[16 * g + i], s[16 * g + i + 1]);
+                mx[g] = fmaxf(a, s[16 * g + 15]);
+              }
             }
             const float top = fmaf(fmax3(fmax3(mx[0], mx[1], mx[2]), fmax3(mx[3], mx[4], mx[5]), fmaxf(mx[6], mx[7])),
                                    sl2, p.delta_log2);
@@ -652,14 +663,19 @@ __global__ void __launch_bounds__(384, 1)
 #pragma unroll
             for (int c = 0; c < 4; ++c) {
               uint32_t pk[16];
+              if (!any[c]) {
 #pragma unroll
-              for (int i = 0; i < 16; ++i) {
-                float x0, x1;
-                f2_unpack(f2_fma(f2_pack(s[32 * c + 2 * i], s[32 * c + 2 * i + 1]), sl2_2, nms_2), x0, x1);
-                x0 = ex2(x0);
-                x1 = ex2(x1);
-                sum2[i & 3] = f2_add(sum2[i & 3], f2_pack(x0, x1));
-                pk[i] = E::pack(x0, x1);
+                for (int i = 0; i < 16; ++i) pk[i] = 0u;
+              } else {
+#pragma unroll
+                for (int i = 0; i < 16; ++i) {
+                  float x0, x1;
+                  f2_unpack(f2_fma(f2_pack(s[32 * c + 2 * i], s[32 * c + 2 * i + 1]), sl2_2, nms_2), x0, x1);
+                  x0 = ex2(x0);
+                  x1 = ex2(x1);
+                  sum2[i & 3] = f2_add(sum2[i & 3], f2_pack(x0, x1));
+                  pk[i] = E::pack(x0, x1);
+                }
               }
               tmem_st16(t_p + c * 16, pk);
             }
