@@ -194,7 +194,15 @@ __global__ void __launch_bounds__(384, 1)
   uint64_t* o_free = o_done + 2;             // [2]
   uint64_t* s_free = o_free + 2;             // [2] the softmax has read S_t (d = 64)
   uint64_t* mma_done = s_free + 2;          // [2] one per MMA issuer
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(mma_done + 2);
+  // windowed kernel, d = 128: K and V have rings of their own (kv_full and
+  // kv_empty are K's), so that K of the next key tile is there while P_bar V of
+  // this one is waited for; and P_bar is handed over in two parts
+  constexpr bool kSplitKV = kWin && !L::kSepP;
+  constexpr bool kParts = kSplitKV && !kVariants;
+  uint64_t* v_full = mma_done + 2;                  // [kStages]
+  uint64_t* v_empty = v_full + (kSplitKV ? L::kStages : 0);
+  uint64_t* p_most = v_empty + (kSplitKV ? L::kStages : 0);   // [2] the first 96 keys of P_bar are written
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(p_most + (kParts ? 2 : 0));
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
 
   const int n_items = p.n_pairs * p.BH;
@@ -209,6 +217,10 @@ __global__ void __launch_bounds__(384, 1)
     for (int s = 0; s < L::kStages; ++s) {
       mbar_init(&kv_full[s], 1);
       mbar_init(&kv_empty[s], L::kSepP ? 2 : 1);
+      if (kSplitKV) {
+        mbar_init(&v_full[s], 1);
+        mbar_init(&v_empty[s], 1);
+      }
     }
     for (int t = 0; t < 2; ++t) {
       mbar_init(&s_full[t], 1);
@@ -216,6 +228,7 @@ __global__ void __launch_bounds__(384, 1)
       mbar_init(&o_done[t], 1);
       mbar_init(&o_free[t], 128);
       mbar_init(&s_free[t], 128);
+      if (kParts) mbar_init(&p_most[t], 128);
     }
     mbar_init(&mma_done[0], 1);
     mbar_init(&mma_done[1], 1);
@@ -278,10 +291,20 @@ __global__ void __launch_bounds__(384, 1)
           for (int j = 0; j < w.nmax; ++j, ++kv_cnt) {
             const uint32_t st = kv_cnt % L::kStages;
             if (!(ok = mbar_wait(&kv_empty[st], ((kv_cnt / L::kStages) & 1) ^ 1, wd))) break;
-            mbar_arrive_expect_tx(&kv_full[st], uint32_t(2 * L::kTileBytes));
             uint8_t* sk = smem + L::kKVOff + st * 2 * L::kTileBytes;
             uint8_t* sv = sk + L::kTileBytes;
             const int key0 = (kWin ? fwd_key_tile(w, j) : j) * 128;
+            if constexpr (kSplitKV) {
+              mbar_arrive_expect_tx(&kv_full[st], uint32_t(L::kTileBytes));
+              for (int s = 0; s < L::kSub; ++s)
+                tma_load_3d(sk + s * L::kSubBytes, &tm_k, &kv_full[st], s * 64, key0, kv_bh, pol_kv);
+              if (!(ok = mbar_wait(&v_empty[st], ((kv_cnt / L::kStages) & 1) ^ 1, wd))) break;
+              mbar_arrive_expect_tx(&v_full[st], uint32_t(L::kTileBytes));
+              for (int s = 0; s < L::kSub; ++s)
+                tma_load_3d(sv + s * L::kSubBytes, &tm_v, &v_full[st], s * 64, key0, kv_bh, pol_kv);
+              continue;
+            }
+            mbar_arrive_expect_tx(&kv_full[st], uint32_t(2 * L::kTileBytes));
             for (int s = 0; s < L::kSub; ++s) {
               tma_load_3d(sk + s * L::kSubBytes, &tm_k, &kv_full[st], s * 64, key0, kv_bh, pol_kv);
               tma_load_3d(sv + s * L::kSubBytes, &tm_v, &kv_full[st], s * 64, key0, kv_bh, pol_kv);
@@ -456,30 +479,56 @@ __global__ void __launch_bounds__(384, 1)
             break;
           tc_fence_after();
           if constexpr (kWin) {
-            // the same order, where a query tile leaves out the key tile that it
-            // does not see; it_cnt counts the P_bar V tiles issued
+            // The same order, where a query tile leaves out the key tile that it
+            // does not see; it_cnt counts the P_bar V tiles issued.  K of the next
+            // key tile has its own barrier and is there before P_bar V of this one
+            // is, and (kParts) P_bar V of the first 96 keys starts while the softmax
+            // still works on the last 32: N = 16384, window 4096: 948 us with
+            // neither, 864 with both; handed over after 64 keys 880, after 32 895.
+            // (The next S tile's second half before P_bar V, over columns that
+            // P_bar leaves free, is 1106: an N = 64 MMA is hardly shorter than an
+            // N = 128 one.)
+            auto issue_pv_part = [&](int t, uint32_t st, bool first, int part) {
+              const uint64_t b = sdesc_add(dv0, st * 2 * L::kTileBytes);
+#pragma unroll
+              for (int k = part ? 6 : 0; k < (part ? 8 : 6); ++k)
+                umma_ts_warp(tmem + L::tm_o(t), tmem + L::tm_p(t) + k * 8, sdesc_add(b, k * 2048), kIdPV,
+                             (!first || k > 0) ? 1u : 0u);
+            };
             const uint32_t pv0[2] = {it_cnt[0], it_cnt[1]};
             for (int t = 0; t < 2; ++t)
               if (takes(w, t, 0)) issue_s(t, kv_cnt % L::kStages);
+            umma_commit_warp(&kv_empty[kv_cnt % L::kStages]);
             if (w.nmax == 1) umma_commit_warp(q_empty);
             for (int j = 0; ok && j < w.nmax; ++j) {
               const uint32_t st = (kv_cnt + j) % L::kStages;
-              const uint32_t nxt = kv_cnt + j + 1;
+              const uint32_t nxt = kv_cnt + j + 1, stn = nxt % L::kStages;
               for (int t = 0; t < 2; ++t) {
+                if (t == 0 && j + 1 < w.nmax && !(ok = wait(&kv_full[stn], (nxt / L::kStages) & 1))) break;
+                if (t == 0 && !(ok = wait(&v_full[st], ((kv_cnt + j) / L::kStages) & 1))) break;
                 if (takes(w, t, j)) {
-                  if (!(ok = wait(&p_full[t], it_cnt[t] & 1))) break;
-                  if (it_cnt[t] == pv0[t] && !(ok = wait(&o_free[t], (ep_cnt[t] & 1) ^ 1))) break;
-                  tc_fence_after();
-                  issue_pv(t, st, int(it_cnt[t] - pv0[t]));
+                  const bool first = it_cnt[t] == pv0[t];
+                  // the first P_bar V of an item overwrites O_t
+                  if (first && !(ok = wait(&o_free[t], (ep_cnt[t] & 1) ^ 1))) break;
+                  if constexpr (kParts) {
+                    if (!(ok = wait(&p_most[t], it_cnt[t] & 1))) break;
+                    tc_fence_after();
+                    issue_pv_part(t, st, first, 0);
+                    if (!(ok = wait(&p_full[t], it_cnt[t] & 1))) break;
+                    tc_fence_after();
+                    issue_pv_part(t, st, first, 1);
+                    umma_commit_warp(&o_done[t]);
+                  } else {
+                    if (!(ok = wait(&p_full[t], it_cnt[t] & 1))) break;
+                    tc_fence_after();
+                    issue_pv(t, st, int(it_cnt[t] - pv0[t]));
+                  }
                   ++it_cnt[t];
                 }
-                if (t == 0 && j + 1 < w.nmax) {
-                  if (!(ok = wait(&kv_full[nxt % L::kStages], (nxt / L::kStages) & 1))) break;
-                  tc_fence_after();
-                }
-                if (t == 1) umma_commit_warp(&kv_empty[st]);
-                if (takes(w, t, j + 1)) issue_s(t, nxt % L::kStages);
-                if (t == 1 && j + 2 == w.nmax) umma_commit_warp(q_empty);
+                if (t == 1) umma_commit_warp(&v_empty[st]);
+                if (takes(w, t, j + 1)) issue_s(t, stn);     // overwrites P_bar_t after P_bar V
+                if (t == 1 && j + 1 < w.nmax) umma_commit_warp(&kv_empty[stn]);
+                if (t == 1 && j + 2 == w.nmax) umma_commit_warp(q_empty);   // the item's last S MMAs are issued
               }
             }
             kv_cnt += w.nmax;
@@ -594,7 +643,8 @@ __global__ void __launch_bounds__(384, 1)
           // repetitions.  P scaled by a power of two is rounded alike in bf16; in
           // fp16 the headroom is smaller, for P below 2^-14 loses bits there.
           // N = 16384, window 4096, d = 128: 1186 us with the exact shift,
-          // 936 us with headroom.
+          // 936 us with headroom.  (A share of the exponentials as a polynomial on
+          // the FMA pipe: 893 us for 1/8 of them, 954 for 1/4, against 864 for none.)
           constexpr float kHeadroom = E::kMmaFmt == 1 ? 8.f : 4.f;
           auto tile = [&](auto edge) {
             // A tile in which some row of the warp does not see every key is taken
@@ -678,6 +728,11 @@ __global__ void __launch_bounds__(384, 1)
                 }
               }
               tmem_st16(t_p + c * 16, pk);
+              if (kParts && c == 2) {                 // O_t is rescaled and 96 keys of P_bar written
+                tmem_st_wait();
+                tc_fence_before();
+                mbar_arrive(&p_most[t]);
+              }
             }
             float ea, eb;
             f2_unpack(f2_add(f2_add(sum2[0], sum2[1]), f2_add(sum2[2], sum2[3])), ea, eb);
