@@ -686,11 +686,19 @@ __global__ void __launch_bounds__(512, 1)
           tmem_ld_wait(r[0]);
           tmem_ld_wait(r[1]);
           const bool diag = p.causal && qt == w.kv_tile;
-          // windowed kernel: queries from `far` of this half on do not see the key
-          int far = 64;
-          if constexpr (kWin)
-            if (w.key0 + kr >= p.sinks) far = min(64, w.key0 + kr + p.window - qt * 128 - 64 * half);
-          if (!__any_sync(0xffffffffu, !key_in || diag || (kWin && far < 64))) {   // no masked entry in this warp
+          // windowed kernel: which of this half's queries see the key, as bits (one
+          // test per entry for both borders: N=8192 d=64 window 1024 500 -> 480 us;
+          // leaving out warps that see nothing gained nothing)
+          [[maybe_unused]] uint32_t see[2] = {0, 0};
+          if constexpr (kWin) {
+            const int from = diag ? kr - 64 * half : 0;
+            const int to = w.key0 + kr < p.sinks ? 64 : w.key0 + kr + p.window - qt * 128 - 64 * half;
+            if (key_in) {
+              see[0] = ~low_bits(from) & low_bits(to);
+              see[1] = ~low_bits(from - 32) & low_bits(to - 32);
+            }
+          }
+          if (!__any_sync(0xffffffffu, kWin ? (see[0] & see[1]) != 0xffffffffu : !key_in || diag)) {   // no masked entry in this warp
 #pragma unroll
             for (int j = 0; j < 16; ++j) {             // 4 queries per shared-memory load of -LSE2
               const float4 nl = *reinterpret_cast<const float4*>(nlse + 4 * j);
@@ -710,7 +718,7 @@ __global__ void __launch_bounds__(512, 1)
             // the key: the exponent is set to -inf, so P = 0 (selected
             // alongside the exponentials; a separate pass that cleared the
             // packed halves afterwards cost ~1600 cycles per diagonal step)
-            const int lim = key_in ? (diag ? kr - 64 * half : 0) : 64;   // queries q < lim are masked
+            [[maybe_unused]] const int lim = key_in ? (diag ? kr - 64 * half : 0) : 64;   // queries q < lim are masked
 #pragma unroll
             for (int j = 0; j < 16; ++j) {
               const float4 nl = *reinterpret_cast<const float4*>(nlse + 4 * j);
@@ -722,11 +730,12 @@ __global__ void __launch_bounds__(512, 1)
                                          __uint_as_float(r[i >> 4][(2 * i + 1) & 31])),
                                  c2, h ? f2_pack(nl.z, nl.w) : f2_pack(nl.x, nl.y)),
                           x0, x1);
-                x0 = (2 * i < lim) ? -__int_as_float(0x7f800000) : x0;
-                x1 = (2 * i + 1 < lim) ? -__int_as_float(0x7f800000) : x1;
                 if constexpr (kWin) {
-                  x0 = (2 * i >= far) ? -__int_as_float(0x7f800000) : x0;
-                  x1 = (2 * i + 1 >= far) ? -__int_as_float(0x7f800000) : x1;
+                  x0 = (see[i >> 4] >> (2 * i & 31) & 1u) ? x0 : -__int_as_float(0x7f800000);
+                  x1 = (see[i >> 4] >> (2 * i + 1 & 31) & 1u) ? x1 : -__int_as_float(0x7f800000);
+                } else {
+                  x0 = (2 * i < lim) ? -__int_as_float(0x7f800000) : x0;
+                  x1 = (2 * i + 1 < lim) ? -__int_as_float(0x7f800000) : x1;
                 }
                 pack_p(i, ex2(x0), ex2(x1));
               }

@@ -515,8 +515,10 @@ __global__ void __launch_bounds__(160, 2)
 
 // Puts a cut unit's partial results together: one CTA per (sequence, query
 // head); units that one CTA finished, and empty sequences, are left alone.
-// Thread t holds four elements of d and a quarter (d = 64: an eighth) of the
-// unit's pieces.
+// A thread holds four elements of d and every fourth (d = 64: eighth) of the
+// unit's pieces, with a running maximum of its own, so that all loads of a unit
+// of up to 16 pieces are in flight together: this kernel is the tail of every
+// call, and a second round trip to the L2 is a quarter of its time.
 template <int D, int NB, typename E>
 __global__ void __launch_bounds__(128) fa_decode_join_kernel(const DecodeParams p) {
   using T = typename E::T;
@@ -524,72 +526,69 @@ __global__ void __launch_bounds__(128) fa_decode_join_kernel(const DecodeParams 
   const float kNegInf = -__int_as_float(0x7f800000);
   constexpr int kCols = D / 4, kRuns = 128 / kCols;
   __shared__ float4 acc[128];
-  __shared__ float run_l[4], run_m[4];
+  __shared__ float run_m[kRuns], run_l[kRuns];
   grid_dep_wait();
   grid_dep_launch();
   const int s = blockIdx.x / p.H, h = blockIdx.x % p.H;
   const int kvh = h / p.group, hg = h % p.group;
   const int unit = kvh * p.blocks + hg / (8 * NB), hd = hg % (8 * NB);
-  const int c0 = p.cum[s], nt = p.cum[s + 1] - c0;
+  const int c0 = p.cum[s], nt = p.cum[s + 1] - c0, all = p.cum[p.S];
   if (nt == 0) return;
-  const long long total = (long long)p.cum[p.S] * p.units;
+  const long long total = (long long)all * p.units;
   const long long xa = (long long)c0 * p.units + (long long)unit * nt, xb = xa + nt;
   const int ca = int(((xa + 1) * p.ctas - 1) / total), cb = int((xb * p.ctas - 1) / total);
   if (ca == cb) return;                     // a whole unit in one stretch
   const size_t slot = 8 * NB * (D + 2);
-  // the CTAs ca .. cb hold one piece each; only the first may begin before xa
-  auto piece = [&](int c) { return p.part + (size_t(c) * 2 + (dec_cut(total, p.ctas, c) >= xa ? 0 : 1)) * slot; };
-  auto has = [&](int c) { return dec_cut(total, p.ctas, c) < dec_cut(total, p.ctas, c + 1); };
-  // maximum and sum over the pieces
-  float m = kNegInf;
-  for (int c = ca + threadIdx.x; c <= cb; c += 128)
-    if (has(c)) m = fmaxf(m, piece(c)[hd]);
-#pragma unroll
-  for (int d = 16; d; d >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, d));
-  if (lane_id() == 0) run_m[warp_id()] = m;
-  __syncthreads();
-  m = fmaxf(fmaxf(run_m[0], run_m[1]), fmaxf(run_m[2], run_m[3]));
-  float l = 0.f;
-  for (int c = ca + threadIdx.x; c <= cb; c += 128)
-    if (has(c)) {
-      const float* x = piece(c);
-      l += x[hd] == kNegInf ? 0.f : x[8 * NB + hd] * ex2(x[hd] - m);
-    }
-#pragma unroll
-  for (int d = 16; d; d >>= 1) l += __shfl_xor_sync(0xffffffffu, l, d);
-  if (lane_id() == 0) run_l[warp_id()] = l;
-  const int dd = (threadIdx.x % kCols) * 4;
+  const int run = threadIdx.x / kCols, dd = (threadIdx.x % kCols) * 4;
+  // CTAs ca .. cb hold one piece each (those whose stretch is empty, none); only
+  // the first may have begun before xa, and then holds it in its second slot
+  float m = kNegInf, l = 0.f;
   float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll 4
-  for (int c = ca + threadIdx.x / kCols; c <= cb; c += kRuns) {
-    if (!has(c)) continue;
-    const float* x = piece(c);
-    const float f = x[hd] == kNegInf ? 0.f : ex2(x[hd] - m);
+  for (int c = ca + run; c <= cb; c += kRuns) {
+    const long long x0 = dec_cut(total, p.ctas, c), x1 = dec_cut(total, p.ctas, c + 1);
+    const float* x = p.part + (size_t(c) * 2 + (x0 >= xa ? 0 : 1)) * slot;
+    if (x0 == x1) continue;
+    const float pm = x[hd], pl = x[8 * NB + hd];
     const float4 b = *reinterpret_cast<const float4*>(x + 16 * NB + hd * D + dd);
+    const float m_new = fmaxf(m, pm), shift = m_new == kNegInf ? 0.f : m_new;
+    const float f = ex2(m - shift), g = ex2(pm - shift);
+    m = m_new;
+    l = fmaf(l, f, pl * g);
+    a.x = fmaf(a.x, f, b.x * g);
+    a.y = fmaf(a.y, f, b.y * g);
+    a.z = fmaf(a.z, f, b.z * g);
+    a.w = fmaf(a.w, f, b.w * g);
+  }
+  acc[threadIdx.x] = a;
+  if (dd == 0) {
+    run_m[run] = m;
+    run_l[run] = l;
+  }
+  __syncthreads();
+  if (run != 0) return;
+  float top = run_m[0];
+#pragma unroll
+  for (int r = 1; r < kRuns; ++r) top = fmaxf(top, run_m[r]);
+  const float shift = top == kNegInf ? 0.f : top;
+  float sum = 0.f;
+  a = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+  for (int r = 0; r < kRuns; ++r) {
+    const float f = ex2(run_m[r] - shift);
+    const float4 b = acc[threadIdx.x + r * kCols];
+    sum = fmaf(run_l[r], f, sum);
     a.x = fmaf(b.x, f, a.x);
     a.y = fmaf(b.y, f, a.y);
     a.z = fmaf(b.z, f, a.z);
     a.w = fmaf(b.w, f, a.w);
   }
-  acc[threadIdx.x] = a;
-  __syncthreads();
-  if (threadIdx.x < kCols) {
-#pragma unroll
-    for (int r = 1; r < kRuns; ++r) {
-      const float4 b = acc[threadIdx.x + r * kCols];
-      a.x += b.x;
-      a.y += b.y;
-      a.z += b.z;
-      a.w += b.w;
-    }
-    l = (run_l[0] + run_l[1]) + (run_l[2] + run_l[3]);
-    const float inv = 1.f / l;
-    uint2 r;
-    r.x = E::pack(a.x * inv, a.y * inv);
-    r.y = E::pack(a.z * inv, a.w * inv);
-    *reinterpret_cast<uint2*>(static_cast<T*>(p.o) + (size_t(s) * p.H + h) * D + dd) = r;
-    if (threadIdx.x == 0) p.lse[size_t(s) * p.H + h] = (m + lg2(l)) * kLn2;
-  }
+  const float inv = 1.f / sum;
+  uint2 r;
+  r.x = E::pack(a.x * inv, a.y * inv);
+  r.y = E::pack(a.z * inv, a.w * inv);
+  *reinterpret_cast<uint2*>(static_cast<T*>(p.o) + (size_t(s) * p.H + h) * D + dd) = r;
+  if (threadIdx.x == 0) p.lse[size_t(s) * p.H + h] = (top + lg2(sum)) * kLn2;
 }
 
 }  // namespace fa

@@ -64,9 +64,6 @@ struct FwdParams {
   int window, sinks;    // windowed kernel: key j is visible where j <= i and (i - j < window or j < sinks)
 };
 
-// A word whose n lowest bits are set (n <= 0: none, n >= 32: all).
-__device__ __forceinline__ uint32_t low_bits(int n) { return n <= 0 ? 0u : 0xffffffffu >> (32 - min(n, 32)); }
-
 template <int D>
 struct FwdLayout {
   static constexpr int kStages = (D == 64) ? 4 : 2;   // K/V ring depth

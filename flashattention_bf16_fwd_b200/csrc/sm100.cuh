@@ -490,6 +490,9 @@ __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
   return r;
 }
 
+// A word whose n lowest bits are set (n <= 0: none, n >= 32: all).
+__device__ __forceinline__ uint32_t low_bits(int n) { return n <= 0 ? 0u : 0xffffffffu >> (32 - min(n, 32)); }
+
 // Work item that a persistent CTA takes in round `rnd` when items are sorted
 // heavy first: the CTAs sweep the sorted list back and forth (0..G-1, then
 // G-1..0, ...), so every CTA receives a mix of heavy and light items.
