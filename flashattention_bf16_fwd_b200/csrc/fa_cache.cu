@@ -153,12 +153,14 @@ int fa_decode(const void* q, const void* k_pages, const void* v_pages, const int
   prm.P = P;
   prm.page = page;
   prm.M = M;
-  prm.box = page % 64 == 0 ? 64 : page % 32 == 0 ? 32 : page % 16 == 0 ? 16 : 8;
+  const int tile = dec_tile(d);
+  prm.box = tile;
+  while (page % prm.box) prm.box /= 2;                    // 8 at least
   prm.z_none = P * Hkv;
   prm.window = window;
   prm.sinks = sinks;
   // two CTAs per SM, or one per tile where there are fewer
-  const long long most = (long long)S * prm.units * (((long long)M * page + kDecTile - 1) / kDecTile);
+  const long long most = (long long)S * prm.units * (((long long)M * page + tile - 1) / tile);
   const int two = 2 * num_sms < kDecMaxCtas ? 2 * num_sms : kDecMaxCtas;
   prm.ctas = int(most < two ? most : two);
   prm.scale_log2 = float(double(scale) * 1.4426950408889634);

@@ -7,7 +7,8 @@
 // by nothing else, so the bound is the bandwidth at which the visible tokens
 // come out of HBM; the arithmetic only has to stay out of the way.
 //
-// Work.  The keys of a sequence are cut into tiles of 64; the tiles of all
+// Work.  The keys of a sequence are cut into tiles of 64 (d = 64: 128, so that a
+// tile is 32 KB of K and V either way); the tiles of all
 // (sequence, key/value head) units, laid end to end, are divided evenly among
 // the CTAs, whatever the lengths: each CTA takes one stretch.  A unit that lies
 // in one stretch is finished there; one that is cut leaves unnormalised
@@ -15,10 +16,11 @@
 // puts together.  The cut depends on lens alone, so that sums always run in
 // the same order.
 //
-// A CTA: warp 4 fetches tiles with TMA, one box per page piece (or per 64 keys)
-// and 64 elements of d, into a ring; warps 0-3 take 16 keys of a tile each and
-// keep a running maximum, sum and O of their own in registers, so that they
-// meet only at the end of a unit.
+// A CTA: warp 4 fetches tiles with TMA into a ring, one box per page (or piece of
+// one) and 64 elements of d, with the queries in front of a unit's first tile;
+// page numbers are read for up to 32 boxes at a time, a batch ahead.  Warps 0-3
+// take a quarter of a tile's keys each and keep a running maximum, sum and O of
+// their own in registers, so that they meet only at the end of a unit.
 // The products run on mma.sync with the keys as rows, S^T = K Q^T and
 // O^T = V^T P^T: 8 query heads are one N = 8 tile, where tcgen05 would spend
 // 128 rows on them.  P enters as P_hi + P_lo, two values of the element format:
@@ -42,31 +44,42 @@ struct DecodeParams {
   long long q_stride;
   int S, H, group, units;   // query heads per K/V head; units per sequence (K/V heads x head blocks)
   int blocks;               // head blocks per K/V head
-  int P, page, M, box;      // box: keys per TMA box (a divisor of 64 and of page)
+  int P, page, M, box;      // box: keys per TMA box (a divisor of the tile and of the page)
   int z_none;               // a third TMA coordinate past the cache: the box reads as zeros
   int window, sinks;
   int ctas;                 // CTAs that the tiles are divided among
   float scale_log2;
 };
 
-constexpr int kDecTile = 64;       // keys per tile
+constexpr int dec_tile(int D) { return D == 64 ? 128 : 64; }   // keys per tile
 constexpr int kDecMaxSeqs = 8192;
 constexpr int kDecMaxCtas = 320;   // two per SM
 
 template <int D, int NB>
 struct DecLayout {
+  static constexpr int kTile = dec_tile(D);
   static constexpr int kSub = D / 64;
-  static constexpr int kSubBytes = kDecTile * 128;           // 64 keys x 64 elements
-  static constexpr int kTileBytes = kSub * kSubBytes;
-  static constexpr int kStages = (D == 64) ? 6 : 3;          // 96 KB of K and V in flight per CTA, two CTAs per SM
+  static constexpr int kSubBytes = kTile * 128;              // a tile's keys x 64 elements
+  static constexpr int kTileBytes = kSub * kSubBytes;        // 16 KB of K, and of V
+  static constexpr int kStages = 3;                          // 96 KB in flight per CTA, two CTAs per SM
   static constexpr int kJoinOff = kStages * 2 * kTileBytes;  // [4 warps][8 NB heads][kJoinRow] floats
-  static constexpr int kJoinCols = 64 / NB;                  // columns of d joined at a time
+  static constexpr int kJoinCols = 32 / NB;                  // columns of d joined at a time
   static constexpr int kJoinRow = kJoinCols + 4;             // rows 4 banks apart: the warps' writes do not collide
   static constexpr int kMlOff = kJoinOff + 4 * 8 * NB * kJoinRow * 4;    // [4 warps][8 NB] m and l
-  static constexpr int kBarOff = kMlOff + 4 * 8 * NB * 2 * 4;
-  static constexpr int kCumOff = kBarOff + 256;              // [S + 1] int32
+  // the queries of a unit, beside the stage of its first tile; 16 heads of 128
+  // would cost the second CTA per SM and are read from global memory
+  static constexpr bool kQSmem = !(NB == 2 && D == 128);
+  static constexpr int kQBytes = kQSmem ? 8 * NB * D * 2 : 0;
+  static constexpr int kQOff = kMlOff + 4 * 8 * NB * 2 * 4;
+  static constexpr int kBarOff = kQOff + kStages * kQBytes;
+  static constexpr int kCumOff = kBarOff + 128;              // [S + 1] tiles before a sequence, then [S] lengths
   static constexpr int kThreads = 160;
-  static size_t bytes(int S) { return size_t(kCumOff) + (size_t(S) + 1) * 4 + 1024; }
+  // lengths are kept beside the tile counts while that leaves two CTAs per SM
+  // (113 KB each; one CTA alone took 84 us for 256 sequences of up to 300 tokens,
+  // two 60 us), and are read from global memory in larger batches
+  static constexpr int kLensMost = 512;
+  static size_t bytes(int S) { return size_t(kCumOff) + (size_t(S) + 1 + (S <= kLensMost ? S : 0)) * 4 + 1024; }
+  static_assert(kCumOff + (2 * kLensMost + 1) * 4 + 1024 <= 113 * 1024, "a second CTA does not fit");
 };
 
 // The tiles of a sequence: those with a sink, then those of the window (all
@@ -77,20 +90,22 @@ struct DecSpan {
   int nt;           // tiles
 };
 
+template <int kTile>
 __device__ __forceinline__ DecSpan dec_span(const DecodeParams& p, int len) {
   DecSpan s;
   s.n = min(max(len, 0), p.M * p.page);
   s.lo = p.window > 0 ? max(0, s.n - p.window) : 0;
   s.sk = min(p.sinks, s.n);
-  const int all = (s.n + kDecTile - 1) / kDecTile;
-  s.st = min((s.sk + kDecTile - 1) / kDecTile, all);
-  s.skip = max(0, s.lo / kDecTile - s.st);
+  const int all = (s.n + kTile - 1) / kTile;
+  s.st = min((s.sk + kTile - 1) / kTile, all);
+  s.skip = max(0, s.lo / kTile - s.st);
   s.nt = all - s.skip;
   return s;
 }
 
+template <int kTile>
 __device__ __forceinline__ int dec_key0(const DecSpan& s, int t) {
-  return (t < s.st ? t : t + s.skip) * kDecTile;
+  return (t < s.st ? t : t + s.skip) * kTile;
 }
 
 // First tile of CTA c's stretch when T tiles are divided among G CTAs.
@@ -148,6 +163,15 @@ __device__ __forceinline__ void mma16816(float (&c)[4], const uint32_t (&a)[4], 
                  : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 
+// An untiled copy of `bytes` (a multiple of 16) from global to shared memory,
+// both 16-byte aligned, completing on `bar`.
+__device__ __forceinline__ void bulk_load(void* dst, const void* src, uint32_t bytes, uint64_t* bar) {
+  asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
+                   smem_u32(dst)),
+               "l"(src), "r"(bytes), "r"(smem_u32(bar))
+               : "memory");
+}
+
 // NB: blocks of 8 query heads that one CTA takes together.
 template <int D, int NB, typename E>
 __global__ void __launch_bounds__(160, 2)
@@ -155,6 +179,7 @@ __global__ void __launch_bounds__(160, 2)
                      const DecodeParams p) {
   using L = DecLayout<D, NB>;
   using T = typename E::T;
+  constexpr int kTile = L::kTile, kRows = kTile / 64;       // kRows: pieces of 16 keys per warp and tile
   constexpr float kLn2 = 0.69314718055994531f;
   const float kNegInf = -__int_as_float(0x7f800000);
   extern __shared__ uint8_t smem_raw[];
@@ -164,8 +189,10 @@ __global__ void __launch_bounds__(160, 2)
   uint64_t* full = reinterpret_cast<uint64_t*>(smem + L::kBarOff);
   uint64_t* empty = full + L::kStages;
   volatile int* abort_flag = reinterpret_cast<volatile int*>(empty + L::kStages);
-  int* warp_sum = reinterpret_cast<int*>(smem + L::kBarOff + 128);
+  int* warp_sum = reinterpret_cast<int*>(smem + L::kBarOff + 64);
   int32_t* cum = reinterpret_cast<int32_t*>(smem + L::kCumOff);
+  int32_t* lens_smem = cum + p.S + 1;
+  const int32_t* lens = p.S <= L::kLensMost ? lens_smem : p.lens;
   const int warp = int(warp_id()), lane = int(lane_id());
 
   if (threadIdx.x == 0) {
@@ -190,7 +217,8 @@ __global__ void __launch_bounds__(160, 2)
   for (int s = s_begin; s < s_end; ++s) {
     const int len = p.lens[s];
     bad |= len < 0 || len > p.M * p.page;
-    mine += dec_span(p, len).nt;
+    if (p.S <= L::kLensMost) lens_smem[s] = len;
+    mine += dec_span<kTile>(p, len).nt;
     cum[s + 1] = mine;
   }
   int before = mine;
@@ -224,52 +252,77 @@ __global__ void __launch_bounds__(160, 2)
   const Watchdog wd{abort_flag, p.dev_error};
   DecWalk w;
   w.start(cum, p.S, p.units, x0);
+  // the query heads of a unit: the first one, and how many
+  auto heads = [&](const DecWalk& u, int& h0, int& nh) {
+    const int kvh = u.unit / p.blocks;
+    h0 = kvh * p.group + (u.unit % p.blocks) * 8 * NB;
+    nh = min(8 * NB, (kvh + 1) * p.group - h0);
+  };
 
   if (warp == 4) {
     // ---------------------------------------------------------------- producer
-    // Lane b fetches box b of a tile (K and V).  The page number of the next
-    // tile's box is read before this tile's buffer is waited for.
-    const int boxes = kDecTile / p.box;
+    // Lanes take the boxes of 32 / boxes tiles at a time, K and V: where their
+    // box begins, and its page.  A batch's page numbers are read while the batch
+    // before it is copied.
+    const int boxes = kTile / p.box, batch = 32 / boxes;
+    const int my_tile = lane / boxes, my_box = lane % boxes;
     const uint64_t pol = l2_policy_evict_first();
     const int hkv = p.units / p.blocks;
-    auto third = [&](const DecWalk& u) {       // the third TMA coordinate of this lane's box
-      if (lane >= boxes) return 0;
-      const DecSpan sp = dec_span(p, p.lens[u.s]);
-      const int key = dec_key0(sp, u.t) + lane * p.box;
-      const bool seen = key < sp.n && (key + p.box > sp.lo || key < sp.sk);
-      if (!seen) return p.z_none;
-      const int id = p.table[size_t(u.s) * p.M + key / p.page];
-      if (id < 0 || id >= p.P) {
-        atomicExch(p.dev_error, kDevErrPages);
-        return p.z_none;
+    int id = 0, row = 0, head = 0;           // this lane's box: page number, row of the page, K/V head
+    bool seen = false;
+    const void* q = nullptr;                 // lane of a tile's first box: the queries to fetch with it
+    uint32_t q_bytes = 0;
+    auto look = [&](int i0) {
+      const int i = i0 + my_tile;
+      q_bytes = 0;
+      seen = false;
+      if (i >= n_tiles) return;
+      DecWalk u;
+      u.start(cum, p.S, p.units, x0 + i);
+      const DecSpan sp = dec_span<kTile>(p, lens[u.s]);
+      const int key = dec_key0<kTile>(sp, u.t) + my_box * p.box;
+      row = key % p.page;
+      head = u.unit / p.blocks;
+      seen = key < sp.n && (key + p.box > sp.lo || key < sp.sk);      // some query sees a key of the box
+      if (seen) id = p.table[size_t(u.s) * p.M + key / p.page];       // not looked at before its batch's turn
+      if (L::kQSmem && my_box == 0 && (i == 0 || u.t == 0)) {
+        int h0, nh;
+        heads(u, h0, nh);
+        q = static_cast<const T*>(p.q) + size_t(u.s) * p.q_stride + size_t(h0) * D;
+        q_bytes = uint32_t(nh) * D * 2;
       }
-      return id * hkv + u.unit / p.blocks;
     };
-    auto second = [&](const DecWalk& u) {
-      const DecSpan sp = dec_span(p, p.lens[u.s]);
-      return (dec_key0(sp, u.t) + lane * p.box) % p.page;
-    };
-    int z = third(w), row = second(w);
+    look(0);
     bool ok = true;
     int i = 0;
-    for (; i < n_tiles; ++i) {
-      const int st = i % L::kStages;
-      ok = __all_sync(0xffffffffu, mbar_wait(&empty[st], ((i / L::kStages) & 1) ^ 1, wd));
-      if (!ok) break;
-      if (lane == 0) mbar_arrive_expect_tx(&full[st], uint32_t(2 * L::kTileBytes));
-      __syncwarp();
-      if (lane < boxes) {
-        uint8_t* sk = smem + st * 2 * L::kTileBytes + lane * p.box * 128;
-#pragma unroll
-        for (int s = 0; s < L::kSub; ++s) {
-          tma_load_3d(sk + s * L::kSubBytes, &tm_k, &full[st], s * 64, row, z, pol);
-          tma_load_3d(sk + L::kTileBytes + s * L::kSubBytes, &tm_v, &full[st], s * 64, row, z, pol);
-        }
+    for (int i0 = 0; ok && i0 < n_tiles; i0 += batch) {
+      if (seen && (id < 0 || id >= p.P)) {
+        seen = false;
+        atomicExch(p.dev_error, kDevErrPages);
       }
-      if (i + 1 < n_tiles) {
-        w.next(cum, p.S, p.units);
-        z = third(w);
-        row = second(w);
+      const int z = seen ? id * hkv + head : p.z_none, r = row;       // unseen and bad pages read as zeros
+      const void* src = q;
+      const uint32_t src_bytes = q_bytes;
+      if (i0 + batch < n_tiles) look(i0 + batch);
+      const int end = min(i0 + batch, n_tiles);
+      for (i = i0; i < end; ++i) {
+        const int st = i % L::kStages;
+        ok = __all_sync(0xffffffffu, mbar_wait(&empty[st], ((i / L::kStages) & 1) ^ 1, wd));
+        if (!ok) break;
+        const bool mine = my_tile == i - i0;
+        if (mine && my_box == 0) {
+          mbar_arrive_expect_tx(&full[st], uint32_t(2 * L::kTileBytes) + src_bytes);
+          if (src_bytes) bulk_load(smem + L::kQOff + st * L::kQBytes, src, src_bytes, &full[st]);
+        }
+        __syncwarp();
+        if (mine) {
+          uint8_t* sk = smem + st * 2 * L::kTileBytes + my_box * p.box * 128;
+#pragma unroll
+          for (int s = 0; s < L::kSub; ++s) {
+            tma_load_3d(sk + s * L::kSubBytes, &tm_k, &full[st], s * 64, r, z, pol);
+            tma_load_3d(sk + L::kTileBytes + s * L::kSubBytes, &tm_v, &full[st], s * 64, r, z, pol);
+          }
+        }
       }
     }
     // given up: the copies in flight still write this CTA's shared memory; wait
@@ -293,24 +346,28 @@ __global__ void __launch_bounds__(160, 2)
   int seg_t0 = 0;
   DecSpan sp{};
   const uint32_t tile0 = smem_u32(smem);
-  const int row_k = warp * 16 + (lane & 15);                          // K: rows of the four matrices
-  const int row_v = warp * 16 + (lane & 7) + ((lane >> 4) << 3);      // V: keys of the four matrices
+  const int row_k = warp * (16 * kRows) + (lane & 15);                          // K: rows of the four matrices
+  const int row_v = warp * (16 * kRows) + (lane & 7) + ((lane >> 4) << 3);      // V: keys of the four matrices
 
   for (int i = 0; i < n_tiles; ++i) {
-    const int kvh = w.unit / p.blocks, h0 = kvh * p.group + (w.unit % p.blocks) * 8 * NB;
-    const int nh = min(8 * NB, (kvh + 1) * p.group - h0);
+    int h0, nh;
+    heads(w, h0, nh);
+    const int st = i % L::kStages;
+    if (ok) ok = __all_sync(0xffffffffu, mbar_wait(&full[st], (i / L::kStages) & 1, wd));
     if (fresh) {
-      sp = dec_span(p, p.lens[w.s]);
+      sp = dec_span<kTile>(p, lens[w.s]);
       seg_t0 = w.t;
-      const T* q = static_cast<const T*>(p.q) + size_t(w.s) * p.q_stride + size_t(h0) * D;
+      // heads past the unit's last are computed from whatever is there and not
+      // stored; no column of S^T or O^T depends on another
+      const T* q = L::kQSmem ? reinterpret_cast<const T*>(smem + L::kQOff + st * L::kQBytes)
+                             : static_cast<const T*>(p.q) + size_t(w.s) * p.q_stride + size_t(h0) * D;
 #pragma unroll
       for (int nb = 0; nb < NB; ++nb) {
-        const bool in = nb * 8 + g < nh;
-        const T* qr = q + (in ? nb * 8 + g : 0) * D + tq * 2;
+        const T* qr = q + (L::kQSmem || nb * 8 + g < nh ? nb * 8 + g : 0) * D + tq * 2;
 #pragma unroll
         for (int k = 0; k < D / 16; ++k) {
-          qf[k][nb][0] = in ? *reinterpret_cast<const uint32_t*>(qr + k * 16) : 0u;
-          qf[k][nb][1] = in ? *reinterpret_cast<const uint32_t*>(qr + k * 16 + 8) : 0u;
+          qf[k][nb][0] = *reinterpret_cast<const uint32_t*>(qr + k * 16);
+          qf[k][nb][1] = *reinterpret_cast<const uint32_t*>(qr + k * 16 + 8);
         }
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
@@ -324,46 +381,53 @@ __global__ void __launch_bounds__(160, 2)
       }
       fresh = false;
     }
-    const int st = i % L::kStages;
-    if (ok) ok = __all_sync(0xffffffffu, mbar_wait(&full[st], (i / L::kStages) & 1, wd));
-    const int key0 = dec_key0(sp, w.t);
-    const int ka = key0 + warp * 16 + g, kb = ka + 8;     // this thread's rows of S^T
     auto seen = [&](int key) { return key < sp.n && (key >= sp.lo || key < sp.sk); };
-    const int kw = key0 + warp * 16;
-    const bool whole = kw + 16 <= sp.n && (kw >= sp.lo || kw + 16 <= sp.sk);
-    const bool none = kw >= sp.n || (kw >= sp.sk && kw + 16 <= sp.lo);
+    const int kw = dec_key0<kTile>(sp, w.t) + warp * (16 * kRows);      // this warp's first key
+    const bool whole = kw + 16 * kRows <= sp.n && (kw >= sp.lo || kw + 16 * kRows <= sp.sk);
+    const bool none = kw >= sp.n || (kw >= sp.sk && kw + 16 * kRows <= sp.lo);
     if (ok && !none) {
       const uint32_t tk = tile0 + st * 2 * L::kTileBytes, tv = tk + L::kTileBytes;
-      float c[NB][4];
+      float c[kRows][NB][4];
 #pragma unroll
-      for (int nb = 0; nb < NB; ++nb)
+      for (int r = 0; r < kRows; ++r)
 #pragma unroll
-        for (int e = 0; e < 4; ++e) c[nb][e] = 0.f;
+        for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) c[r][nb][e] = 0.f;
 #pragma unroll
       for (int k = 0; k < D / 16; ++k) {
-        uint32_t a[4];
-        ldsm4(a, tk + (k >> 2) * L::kSubBytes + row_k * 128 + ((((k & 3) * 2 + (lane >> 4)) ^ (row_k & 7)) << 4));
 #pragma unroll
-        for (int nb = 0; nb < NB; ++nb) mma16816<E>(c[nb], a, qf[k][nb][0], qf[k][nb][1]);
-      }
-      if (!whole) {
-        const bool sa = seen(ka), sb = seen(kb);
+        for (int r = 0; r < kRows; ++r) {
+          uint32_t a[4];
+          ldsm4(a, tk + (k >> 2) * L::kSubBytes + (row_k + 16 * r) * 128 +
+                       ((((k & 3) * 2 + (lane >> 4)) ^ (row_k & 7)) << 4));
 #pragma unroll
-        for (int nb = 0; nb < NB; ++nb) {
-          c[nb][0] = sa ? c[nb][0] : kNegInf;
-          c[nb][1] = sa ? c[nb][1] : kNegInf;
-          c[nb][2] = sb ? c[nb][2] : kNegInf;
-          c[nb][3] = sb ? c[nb][3] : kNegInf;
+          for (int nb = 0; nb < NB; ++nb) mma16816<E>(c[r][nb], a, qf[k][nb][0], qf[k][nb][1]);
         }
       }
-      uint32_t ph[NB][2], pl[NB][2];
+      if (!whole) {
+#pragma unroll
+        for (int r = 0; r < kRows; ++r) {
+          const bool sa = seen(kw + 16 * r + g), sb = seen(kw + 16 * r + g + 8);
+#pragma unroll
+          for (int nb = 0; nb < NB; ++nb) {
+            c[r][nb][0] = sa ? c[r][nb][0] : kNegInf;
+            c[r][nb][1] = sa ? c[r][nb][1] : kNegInf;
+            c[r][nb][2] = sb ? c[r][nb][2] : kNegInf;
+            c[r][nb][3] = sb ? c[r][nb][3] : kNegInf;
+          }
+        }
+      }
+      uint32_t ph[kRows][NB][2], pl[kRows][NB][2];
       bool moved = false;
       float alpha[NB][2];
 #pragma unroll
       for (int nb = 0; nb < NB; ++nb) {
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
-          float mx = fmaxf(c[nb][e], c[nb][e + 2]);
+          float mx = fmaxf(c[0][nb][e], c[0][nb][e + 2]);
+#pragma unroll
+          for (int r = 1; r < kRows; ++r) mx = fmaxf(mx, fmaxf(c[r][nb][e], c[r][nb][e + 2]));
           mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 4));
           mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 8));
           mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 16));
@@ -372,18 +436,25 @@ __global__ void __launch_bounds__(160, 2)
           alpha[nb][e] = ex2(ms[nb][e] - shift);           // 0 where nothing was seen before
           moved |= m_new != ms[nb][e];
           ms[nb][e] = m_new;
-          c[nb][e] = ex2(fmaf(c[nb][e], p.scale_log2, -shift));
-          c[nb][e + 2] = ex2(fmaf(c[nb][e + 2], p.scale_log2, -shift));
-          l[nb][e] = fmaf(l[nb][e], alpha[nb][e], c[nb][e] + c[nb][e + 2]);
+          float sum = 0.f;
+#pragma unroll
+          for (int r = 0; r < kRows; ++r) {
+            c[r][nb][e] = ex2(fmaf(c[r][nb][e], p.scale_log2, -shift));
+            c[r][nb][e + 2] = ex2(fmaf(c[r][nb][e + 2], p.scale_log2, -shift));
+            sum += c[r][nb][e] + c[r][nb][e + 2];
+          }
+          l[nb][e] = fmaf(l[nb][e], alpha[nb][e], sum);
         }
 #pragma unroll
-        for (int hv = 0; hv < 2; ++hv) {                    // keys 0-7, 8-15 of the warp's 16
-          const float a = c[nb][2 * hv], b = c[nb][2 * hv + 1];
-          const uint32_t hi = E::pack(a, b);
-          const float2 r = E::unpack(hi);
-          ph[nb][hv] = transpose8(hi);
-          pl[nb][hv] = transpose8(E::pack(a - r.x, b - r.y));
-        }
+        for (int r = 0; r < kRows; ++r)
+#pragma unroll
+          for (int hv = 0; hv < 2; ++hv) {                  // keys 0-7, 8-15 of the 16
+            const float a = c[r][nb][2 * hv], b = c[r][nb][2 * hv + 1];
+            const uint32_t hi = E::pack(a, b);
+            const float2 q = E::unpack(hi);
+            ph[r][nb][hv] = transpose8(hi);
+            pl[r][nb][hv] = transpose8(E::pack(a - q.x, b - q.y));
+          }
       }
       if (__any_sync(0xffffffffu, moved)) {
 #pragma unroll
@@ -393,27 +464,30 @@ __global__ void __launch_bounds__(160, 2)
 #pragma unroll
             for (int e = 0; e < 4; ++e) o[k][nb][e] *= alpha[nb][e & 1];
       }
-      // hidden keys: P is 0, and V is cleared because 0 times what lies there
-      // need not be 0
-      uint32_t keep0 = 0xffffffffu, keep1 = 0xffffffffu;
-      if (!whole) {
-        const int kk = kw + tq * 2;
-        keep0 = (seen(kk) ? 0xffffu : 0u) | (seen(kk + 1) ? 0xffff0000u : 0u);
-        keep1 = (seen(kk + 8) ? 0xffffu : 0u) | (seen(kk + 9) ? 0xffff0000u : 0u);
-      }
 #pragma unroll
-      for (int k = 0; k < D / 16; ++k) {
-        uint32_t a[4];
-        ldsm4_t(a, tv + (k >> 2) * L::kSubBytes + row_v * 128 +
-                       ((((k & 3) * 2 + ((lane >> 3) & 1)) ^ (row_v & 7)) << 4));
-        a[0] &= keep0;
-        a[1] &= keep0;
-        a[2] &= keep1;
-        a[3] &= keep1;
+      for (int r = 0; r < kRows; ++r) {
+        // hidden keys: P is 0, and V is cleared because 0 times what lies there
+        // need not be 0
+        uint32_t keep0 = 0xffffffffu, keep1 = 0xffffffffu;
+        if (!whole) {
+          const int kk = kw + 16 * r + tq * 2;
+          keep0 = (seen(kk) ? 0xffffu : 0u) | (seen(kk + 1) ? 0xffff0000u : 0u);
+          keep1 = (seen(kk + 8) ? 0xffffu : 0u) | (seen(kk + 9) ? 0xffff0000u : 0u);
+        }
 #pragma unroll
-        for (int nb = 0; nb < NB; ++nb) {
-          mma16816<E>(o[k][nb], a, ph[nb][0], ph[nb][1]);
-          mma16816<E>(o[k][nb], a, pl[nb][0], pl[nb][1]);
+        for (int k = 0; k < D / 16; ++k) {
+          uint32_t a[4];
+          ldsm4_t(a, tv + (k >> 2) * L::kSubBytes + (row_v + 16 * r) * 128 +
+                         ((((k & 3) * 2 + ((lane >> 3) & 1)) ^ (row_v & 7)) << 4));
+          a[0] &= keep0;
+          a[1] &= keep0;
+          a[2] &= keep1;
+          a[3] &= keep1;
+#pragma unroll
+          for (int nb = 0; nb < NB; ++nb) {
+            mma16816<E>(o[k][nb], a, ph[r][nb][0], ph[r][nb][1]);
+            mma16816<E>(o[k][nb], a, pl[r][nb][0], pl[r][nb][1]);
+          }
         }
       }
     }
@@ -455,8 +529,9 @@ __global__ void __launch_bounds__(160, 2)
         }
       const bool done = unit_end && seg_t0 == 0;       // the unit lies in this stretch
       float* part = p.part + (size_t(blockIdx.x) * 2 + (first ? 0 : 1)) * (8 * NB * (D + 2));
-      const int hd = int(threadIdx.x) / (L::kJoinCols / 4);          // this thread's head and four columns
-      const int col = (int(threadIdx.x) % (L::kJoinCols / 4)) * 4;
+      static_assert(8 * NB * L::kJoinCols == 2 * 128, "128 threads take two columns each");
+      const int hd = int(threadIdx.x) / (L::kJoinCols / 2);          // this thread's head and two columns
+      const int col = (int(threadIdx.x) % (L::kJoinCols / 2)) * 2;
       float m = kNegInf, lsum = 0.f;
 #pragma unroll
       for (int v = 0; v < 4; ++v) m = fmaxf(m, ml[(v * 8 * NB + hd) * 2]);
@@ -477,24 +552,20 @@ __global__ void __launch_bounds__(160, 2)
               join[(warp * 8 * NB + nb * 8 + tq * 2 + (e & 1)) * L::kJoinRow + k * 16 + g + (e >> 1) * 8] =
                   o[ch * kPer + k][nb][e];
         named_bar_sync(1, 128);
-        float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
+        float2 a = make_float2(0.f, 0.f);
 #pragma unroll
         for (int v = 0; v < 4; ++v) {
-          const float4 b = *reinterpret_cast<const float4*>(join + (v * 8 * NB + hd) * L::kJoinRow + col);
+          const float2 b = *reinterpret_cast<const float2*>(join + (v * 8 * NB + hd) * L::kJoinRow + col);
           a.x += b.x;
           a.y += b.y;
-          a.z += b.z;
-          a.w += b.w;
         }
         const int dd = ch * L::kJoinCols + col;
         if (!done) {
-          *reinterpret_cast<float4*>(part + 16 * NB + hd * D + dd) = a;
+          *reinterpret_cast<float2*>(part + 16 * NB + hd * D + dd) = a;
         } else if (hd < nh) {
           const float inv = 1.f / lsum;
-          uint2 r;
-          r.x = E::pack(a.x * inv, a.y * inv);
-          r.y = E::pack(a.z * inv, a.w * inv);
-          *reinterpret_cast<uint2*>(static_cast<T*>(p.o) + (size_t(w.s) * p.H + h0 + hd) * D + dd) = r;
+          *reinterpret_cast<uint32_t*>(static_cast<T*>(p.o) + (size_t(w.s) * p.H + h0 + hd) * D + dd) =
+              E::pack(a.x * inv, a.y * inv);
         }
         named_bar_sync(1, 128);
       }
