@@ -159,8 +159,8 @@ int fa_decode(const void* q, const void* k_pages, const void* v_pages, const int
   prm.z_none = P * Hkv;
   prm.window = window;
   prm.sinks = sinks;
-  // two CTAs per SM, or one per tile where there are fewer
-  const long long most = (long long)S * prm.units * (((long long)M * page + tile - 1) / tile);
+  // two CTAs per SM, or one per place where there are fewer
+  const long long most = (long long)S * prm.units * (((long long)M * page + tile - 1) / tile + 1);
   const int two = 2 * num_sms < kDecMaxCtas ? 2 * num_sms : kDecMaxCtas;
   prm.ctas = int(most < two ? most : two);
   prm.scale_log2 = float(double(scale) * 1.4426950408889634);

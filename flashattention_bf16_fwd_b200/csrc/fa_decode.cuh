@@ -8,13 +8,16 @@
 // come out of HBM; the arithmetic only has to stay out of the way.
 //
 // Work.  The keys of a sequence are cut into tiles of 64 (d = 64: 128, so that a
-// tile is 32 KB of K and V either way); the tiles of all
-// (sequence, key/value head) units, laid end to end, are divided evenly among
-// the CTAs, whatever the lengths: each CTA takes one stretch.  A unit that lies
-// in one stretch is finished there; one that is cut leaves unnormalised
-// partial results (O, m, l), at most two per CTA, which fa_decode_join_kernel
-// puts together.  The cut depends on lens alone, so that sums always run in
-// the same order.
+// tile is 32 KB of K and V either way); the tiles of all (sequence, key/value
+// head) units, laid end to end, are divided evenly among the CTAs, whatever the
+// lengths: each CTA takes one stretch.  A place without a tile follows each
+// unit's tiles, for finishing a unit costs about as much as a tile (that, and
+// joining the warps' O in a stage at once instead of 32 columns at a time: 256
+// sequences of up to 300 tokens, H = 32 over Hkv = 8, d = 128: 60 -> 53 us).  A
+// unit that lies in one stretch is finished there; one that is cut leaves
+// unnormalised partial results (O, m, l), at most two per CTA, which
+// fa_decode_join_kernel puts together.  The cut depends on lens alone, so that
+// sums always run in the same order.
 //
 // A CTA: warp 4 fetches tiles with TMA into a ring, one box per page (or piece of
 // one) and 64 elements of d, with the queries in front of a unit's first tile;
@@ -38,7 +41,7 @@ struct DecodeParams {
   const int32_t* lens;   // [S]
   void* o;               // [S, H, D]
   float* lse;            // [S, H]
-  int32_t* cum;          // workspace: [S + 1] tiles before each sequence
+  int32_t* cum;          // workspace: [S + 1] places of a unit of each earlier sequence
   float* part;           // workspace: [2 * CTAs] partial results
   int* dev_error;
   long long q_stride;
@@ -62,19 +65,21 @@ struct DecLayout {
   static constexpr int kSubBytes = kTile * 128;              // a tile's keys x 64 elements
   static constexpr int kTileBytes = kSub * kSubBytes;        // 16 KB of K, and of V
   static constexpr int kStages = 3;                          // 96 KB in flight per CTA, two CTAs per SM
-  static constexpr int kJoinOff = kStages * 2 * kTileBytes;  // [4 warps][8 NB heads][kJoinRow] floats
-  static constexpr int kJoinCols = 32 / NB;                  // columns of d joined at a time
+  // the warps' O are joined in the stage that held the unit's last tile, this
+  // many columns of d at a time: [4 warps][8 NB heads][kJoinRow] floats
+  static constexpr int kJoinCols = NB == 1 ? D : 64;
   static constexpr int kJoinRow = kJoinCols + 4;             // rows 4 banks apart: the warps' writes do not collide
-  static constexpr int kMlOff = kJoinOff + 4 * 8 * NB * kJoinRow * 4;    // [4 warps][8 NB] m and l
+  static_assert(4 * 8 * NB * kJoinRow * 4 <= 2 * kTileBytes, "the join does not fit a stage");
+  static constexpr int kMlOff = kStages * 2 * kTileBytes;    // [4 warps][8 NB] m and l
   // the queries of a unit, beside the stage of its first tile; 16 heads of 128
   // would cost the second CTA per SM and are read from global memory
   static constexpr bool kQSmem = !(NB == 2 && D == 128);
   static constexpr int kQBytes = kQSmem ? 8 * NB * D * 2 : 0;
   static constexpr int kQOff = kMlOff + 4 * 8 * NB * 2 * 4;
   static constexpr int kBarOff = kQOff + kStages * kQBytes;
-  static constexpr int kCumOff = kBarOff + 128;              // [S + 1] tiles before a sequence, then [S] lengths
+  static constexpr int kCumOff = kBarOff + 128;              // [S + 1] as DecodeParams::cum, then [S] lengths
   static constexpr int kThreads = 160;
-  // lengths are kept beside the tile counts while that leaves two CTAs per SM
+  // lengths are kept beside them while that leaves two CTAs per SM
   // (113 KB each; one CTA alone took 84 us for 256 sequences of up to 300 tokens,
   // two 60 us), and are read from global memory in larger batches
   static constexpr int kLensMost = 512;
@@ -108,12 +113,13 @@ __device__ __forceinline__ int dec_key0(const DecSpan& s, int t) {
   return (t < s.st ? t : t + s.skip) * kTile;
 }
 
-// First tile of CTA c's stretch when T tiles are divided among G CTAs.
+// First place of CTA c's stretch when T places are divided among G CTAs.
 __device__ __forceinline__ long long dec_cut(long long T, int G, int c) { return T * c / G; }
 
-// A walk over one CTA's stretch of tiles.
+// A place in the sequence of all units' tiles: tile t of a unit of sequence s,
+// or, where t is the unit's number of tiles, the place without one behind it.
 struct DecWalk {
-  int s, unit, t;
+  int s, unit, t, nt;
   __device__ __forceinline__ void start(const int32_t* cum, int S, int units, long long x) {
     int a = 0, b = S;               // the last s with cum[s] * units <= x and tiles of its own
     while (b - a > 1) {
@@ -121,17 +127,19 @@ struct DecWalk {
       if ((long long)cum[mid] * units <= x) a = mid; else b = mid;
     }
     s = a;
-    const int nt = cum[s + 1] - cum[s];
+    const int places = cum[s + 1] - cum[s];
     const int r = int(x - (long long)cum[s] * units);
-    unit = nt > 0 ? r / nt : 0;
-    t = nt > 0 ? r % nt : 0;
+    unit = r / places;
+    t = r % places;
+    nt = places - 1;
   }
   __device__ __forceinline__ void next(const int32_t* cum, int S, int units) {
-    if (++t < cum[s + 1] - cum[s]) return;
+    if (++t <= nt) return;
     t = 0;
     if (++unit < units) return;
     unit = 0;
     do ++s; while (s < S && cum[s + 1] == cum[s]);
+    nt = s < S ? cum[s + 1] - cum[s] - 1 : 0;
   }
 };
 
@@ -184,7 +192,6 @@ __global__ void __launch_bounds__(160, 2)
   const float kNegInf = -__int_as_float(0x7f800000);
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-  float* join = reinterpret_cast<float*>(smem + L::kJoinOff);
   float* ml = reinterpret_cast<float*>(smem + L::kMlOff);
   uint64_t* full = reinterpret_cast<uint64_t*>(smem + L::kBarOff);
   uint64_t* empty = full + L::kStages;
@@ -208,8 +215,7 @@ __global__ void __launch_bounds__(160, 2)
   grid_dep_wait();
   grid_dep_launch();
 
-  // cum: tiles before each sequence.  Each thread sums a run of sequences, the
-  // runs are scanned over the CTA.
+  // cum: each thread sums a run of sequences, the runs are scanned over the CTA.
   const int run = (p.S + L::kThreads - 1) / L::kThreads;
   const int s_begin = min(p.S, int(threadIdx.x) * run), s_end = min(p.S, s_begin + run);
   int mine = 0;
@@ -218,7 +224,8 @@ __global__ void __launch_bounds__(160, 2)
     const int len = p.lens[s];
     bad |= len < 0 || len > p.M * p.page;
     if (p.S <= L::kLensMost) lens_smem[s] = len;
-    mine += dec_span<kTile>(p, len).nt;
+    const int nt = dec_span<kTile>(p, len).nt;
+    mine += nt ? nt + 1 : 0;
     cum[s + 1] = mine;
   }
   int before = mine;
@@ -247,8 +254,8 @@ __global__ void __launch_bounds__(160, 2)
 
   const long long total = (long long)cum[p.S] * p.units;
   const long long x0 = dec_cut(total, p.ctas, blockIdx.x), x1 = dec_cut(total, p.ctas, blockIdx.x + 1);
-  const int n_tiles = int(x1 - x0);
-  if (n_tiles == 0) return;
+  const int n = int(x1 - x0);
+  if (n == 0) return;
   const Watchdog wd{abort_flag, p.dev_error};
   DecWalk w;
   w.start(cum, p.S, p.units, x0);
@@ -261,31 +268,33 @@ __global__ void __launch_bounds__(160, 2)
 
   if (warp == 4) {
     // ---------------------------------------------------------------- producer
-    // Lanes take the boxes of 32 / boxes tiles at a time, K and V: where their
+    // Lanes take the boxes of 32 / boxes places at a time, K and V: where their
     // box begins, and its page.  A batch's page numbers are read while the batch
     // before it is copied.
     const int boxes = kTile / p.box, batch = 32 / boxes;
-    const int my_tile = lane / boxes, my_box = lane % boxes;
+    const int my_place = lane / boxes, my_box = lane % boxes;
     const uint64_t pol = l2_policy_evict_first();
     const int hkv = p.units / p.blocks;
     int id = 0, row = 0, head = 0;           // this lane's box: page number, row of the page, K/V head
-    bool seen = false;
+    bool seen = false, real = false;         // a query sees a key of the box; the place has a tile
     const void* q = nullptr;                 // lane of a tile's first box: the queries to fetch with it
     uint32_t q_bytes = 0;
     auto look = [&](int i0) {
-      const int i = i0 + my_tile;
+      const int i = i0 + my_place;
       q_bytes = 0;
-      seen = false;
-      if (i >= n_tiles) return;
+      seen = real = false;
+      if (i >= n) return;
       DecWalk u;
       u.start(cum, p.S, p.units, x0 + i);
+      real = u.t < u.nt;
+      if (!real) return;
       const DecSpan sp = dec_span<kTile>(p, lens[u.s]);
       const int key = dec_key0<kTile>(sp, u.t) + my_box * p.box;
       row = key % p.page;
       head = u.unit / p.blocks;
-      seen = key < sp.n && (key + p.box > sp.lo || key < sp.sk);      // some query sees a key of the box
+      seen = key < sp.n && (key + p.box > sp.lo || key < sp.sk);
       if (seen) id = p.table[size_t(u.s) * p.M + key / p.page];       // not looked at before its batch's turn
-      if (L::kQSmem && my_box == 0 && (i == 0 || u.t == 0)) {
+      if (L::kQSmem && my_box == 0 && (i == 0 || u.t == 0)) {          // the unit's first tile here
         int h0, nh;
         heads(u, h0, nh);
         q = static_cast<const T*>(p.q) + size_t(u.s) * p.q_stride + size_t(h0) * D;
@@ -294,22 +303,22 @@ __global__ void __launch_bounds__(160, 2)
     };
     look(0);
     bool ok = true;
-    int i = 0;
-    for (int i0 = 0; ok && i0 < n_tiles; i0 += batch) {
+    int i = 0;                               // tiles fetched
+    for (int i0 = 0; ok && i0 < n; i0 += batch) {
       if (seen && (id < 0 || id >= p.P)) {
         seen = false;
         atomicExch(p.dev_error, kDevErrPages);
       }
       const int z = seen ? id * hkv + head : p.z_none, r = row;       // unseen and bad pages read as zeros
       const void* src = q;
-      const uint32_t src_bytes = q_bytes;
-      if (i0 + batch < n_tiles) look(i0 + batch);
-      const int end = min(i0 + batch, n_tiles);
-      for (i = i0; i < end; ++i) {
+      const uint32_t src_bytes = q_bytes, tiles = __ballot_sync(0xffffffffu, real && my_box == 0);
+      if (i0 + batch < n) look(i0 + batch);
+      for (int b = 0; b < batch; ++b) {
+        if (!(tiles >> (b * boxes) & 1u)) continue;
         const int st = i % L::kStages;
         ok = __all_sync(0xffffffffu, mbar_wait(&empty[st], ((i / L::kStages) & 1) ^ 1, wd));
         if (!ok) break;
-        const bool mine = my_tile == i - i0;
+        const bool mine = my_place == b;
         if (mine && my_box == 0) {
           mbar_arrive_expect_tx(&full[st], uint32_t(2 * L::kTileBytes) + src_bytes);
           if (src_bytes) bulk_load(smem + L::kQOff + st * L::kQBytes, src, src_bytes, &full[st]);
@@ -323,6 +332,7 @@ __global__ void __launch_bounds__(160, 2)
             tma_load_3d(sk + L::kTileBytes + s * L::kSubBytes, &tm_v, &full[st], s * 64, r, z, pol);
           }
         }
+        ++i;
       }
     }
     // given up: the copies in flight still write this CTA's shared memory; wait
@@ -342,14 +352,15 @@ __global__ void __launch_bounds__(160, 2)
   uint32_t qf[D / 16][NB][2];
   float ms[NB][2], l[NB][2], o[D / 16][NB][4];
   bool ok = true, fresh = true;
-  bool first = true;                  // the stretch's first segment: partial slot 0
-  int seg_t0 = 0;
+  int seg_t0 = 0;                     // the unit's first tile in this stretch
   DecSpan sp{};
   const uint32_t tile0 = smem_u32(smem);
   const int row_k = warp * (16 * kRows) + (lane & 15);                          // K: rows of the four matrices
   const int row_v = warp * (16 * kRows) + (lane & 7) + ((lane >> 4) << 3);      // V: keys of the four matrices
 
-  for (int i = 0; i < n_tiles; ++i) {
+  int i = 0;                          // tiles taken
+  for (int x = 0; x < n; ++x, w.next(cum, p.S, p.units)) {
+    if (w.t == w.nt) continue;        // the place behind a unit
     int h0, nh;
     heads(w, h0, nh);
     const int st = i % L::kStages;
@@ -491,96 +502,105 @@ __global__ void __launch_bounds__(160, 2)
         }
       }
     }
-    __syncwarp();
-    if (lane == 0) mbar_arrive(&empty[st]);
+    ++i;
+    const bool unit_end = w.t + 1 == w.nt;
+    if (!unit_end && x + 1 < n) {
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&empty[st]);
+      continue;
+    }
 
-    const bool unit_end = w.t + 1 == sp.nt;
-    if (unit_end || i + 1 == n_tiles) {
-      // the four warps' results of this segment, joined
+    // The unit's end, or the stretch's: the four warps' results are joined.
 #pragma unroll
-      for (int nb = 0; nb < NB; ++nb)
+    for (int nb = 0; nb < NB; ++nb)
 #pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          float x = l[nb][e];
-          x += __shfl_xor_sync(0xffffffffu, x, 4);
-          x += __shfl_xor_sync(0xffffffffu, x, 8);
-          x += __shfl_xor_sync(0xffffffffu, x, 16);
-          if (g == 0) {
-            const int hd = nb * 8 + tq * 2 + e;
-            ml[(warp * 8 * NB + hd) * 2] = ms[nb][e];
-            ml[(warp * 8 * NB + hd) * 2 + 1] = x;
-          }
-        }
-      named_bar_sync(1, 128);
-#pragma unroll
-      for (int nb = 0; nb < NB; ++nb)
-#pragma unroll
-        for (int e = 0; e < 2; ++e) {
+      for (int e = 0; e < 2; ++e) {
+        float y = l[nb][e];
+        y += __shfl_xor_sync(0xffffffffu, y, 4);
+        y += __shfl_xor_sync(0xffffffffu, y, 8);
+        y += __shfl_xor_sync(0xffffffffu, y, 16);
+        if (g == 0) {
           const int hd = nb * 8 + tq * 2 + e;
-          float m = kNegInf;
-#pragma unroll
-          for (int v = 0; v < 4; ++v) m = fmaxf(m, ml[(v * 8 * NB + hd) * 2]);
-          const float f = ms[nb][e] == kNegInf ? 0.f : ex2(ms[nb][e] - m);
-#pragma unroll
-          for (int k = 0; k < D / 16; ++k) {
-            o[k][nb][e] *= f;
-            o[k][nb][e + 2] *= f;
-          }
+          ml[(warp * 8 * NB + hd) * 2] = ms[nb][e];
+          ml[(warp * 8 * NB + hd) * 2 + 1] = y;
         }
-      const bool done = unit_end && seg_t0 == 0;       // the unit lies in this stretch
-      float* part = p.part + (size_t(blockIdx.x) * 2 + (first ? 0 : 1)) * (8 * NB * (D + 2));
-      static_assert(8 * NB * L::kJoinCols == 2 * 128, "128 threads take two columns each");
-      const int hd = int(threadIdx.x) / (L::kJoinCols / 2);          // this thread's head and two columns
-      const int col = (int(threadIdx.x) % (L::kJoinCols / 2)) * 2;
-      float m = kNegInf, lsum = 0.f;
-#pragma unroll
-      for (int v = 0; v < 4; ++v) m = fmaxf(m, ml[(v * 8 * NB + hd) * 2]);
-#pragma unroll
-      for (int v = 0; v < 4; ++v) {
-        const float mv = ml[(v * 8 * NB + hd) * 2];
-        lsum += mv == kNegInf ? 0.f : ml[(v * 8 * NB + hd) * 2 + 1] * ex2(mv - m);
       }
+    named_bar_sync(1, 128);           // m and l are written, and all warps are done with the stage
+    float* join = reinterpret_cast<float*>(smem + st * 2 * L::kTileBytes);
 #pragma unroll
-      for (int ch = 0; ch < D / L::kJoinCols; ++ch) {
-        constexpr int kPer = L::kJoinCols / 16;            // 16-wide pieces of d per round
+    for (int nb = 0; nb < NB; ++nb)
 #pragma unroll
-        for (int k = 0; k < kPer; ++k)
+      for (int e = 0; e < 2; ++e) {
+        const int hd = nb * 8 + tq * 2 + e;
+        float m = kNegInf;
 #pragma unroll
-          for (int nb = 0; nb < NB; ++nb)
+        for (int v = 0; v < 4; ++v) m = fmaxf(m, ml[(v * 8 * NB + hd) * 2]);
+        const float f = ms[nb][e] == kNegInf ? 0.f : ex2(ms[nb][e] - m);
 #pragma unroll
-            for (int e = 0; e < 4; ++e)
-              join[(warp * 8 * NB + nb * 8 + tq * 2 + (e & 1)) * L::kJoinRow + k * 16 + g + (e >> 1) * 8] =
-                  o[ch * kPer + k][nb][e];
-        named_bar_sync(1, 128);
-        float2 a = make_float2(0.f, 0.f);
+        for (int k = 0; k < D / 16; ++k) {
+          o[k][nb][e] *= f;
+          o[k][nb][e + 2] *= f;
+        }
+      }
+    const bool done = unit_end && seg_t0 == 0;       // the unit lies in this stretch
+    // the first slot belongs to a unit that began in an earlier stretch, or with this one
+    float* part = p.part + (size_t(blockIdx.x) * 2 + (x - w.t <= 0 ? 0 : 1)) * (8 * NB * (D + 2));
+#pragma unroll
+    for (int ch = 0; ch < D / L::kJoinCols; ++ch) {
+      constexpr int kPer = L::kJoinCols / 16;        // 16-wide pieces of d at a time
+#pragma unroll
+      for (int k = 0; k < kPer; ++k)
+#pragma unroll
+        for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            join[(warp * 8 * NB + nb * 8 + tq * 2 + (e & 1)) * L::kJoinRow + k * 16 + g + (e >> 1) * 8] =
+                o[ch * kPer + k][nb][e];
+      named_bar_sync(1, 128);
+      constexpr int kItems = 8 * NB * L::kJoinCols / 4;   // four columns of a head
+#pragma unroll
+      for (int it = int(threadIdx.x); it < kItems; it += 128) {
+        const int hd = it / (L::kJoinCols / 4), col = it % (L::kJoinCols / 4) * 4;
+        float m = kNegInf, lsum = 0.f;
+#pragma unroll
+        for (int v = 0; v < 4; ++v) m = fmaxf(m, ml[(v * 8 * NB + hd) * 2]);
 #pragma unroll
         for (int v = 0; v < 4; ++v) {
-          const float2 b = *reinterpret_cast<const float2*>(join + (v * 8 * NB + hd) * L::kJoinRow + col);
+          const float mv = ml[(v * 8 * NB + hd) * 2];
+          lsum += mv == kNegInf ? 0.f : ml[(v * 8 * NB + hd) * 2 + 1] * ex2(mv - m);
+        }
+        float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+        for (int v = 0; v < 4; ++v) {
+          const float4 b = *reinterpret_cast<const float4*>(join + (v * 8 * NB + hd) * L::kJoinRow + col);
           a.x += b.x;
           a.y += b.y;
+          a.z += b.z;
+          a.w += b.w;
         }
         const int dd = ch * L::kJoinCols + col;
         if (!done) {
-          *reinterpret_cast<float2*>(part + 16 * NB + hd * D + dd) = a;
+          *reinterpret_cast<float4*>(part + 16 * NB + hd * D + dd) = a;
+          if (dd == 0) {
+            part[hd] = m;
+            part[8 * NB + hd] = lsum;
+          }
         } else if (hd < nh) {
           const float inv = 1.f / lsum;
-          *reinterpret_cast<uint32_t*>(static_cast<T*>(p.o) + (size_t(w.s) * p.H + h0 + hd) * D + dd) =
-              E::pack(a.x * inv, a.y * inv);
-        }
-        named_bar_sync(1, 128);
-      }
-      if (col == 0) {
-        if (!done) {
-          part[hd] = m;
-          part[8 * NB + hd] = lsum;
-        } else if (hd < nh) {
-          p.lse[size_t(w.s) * p.H + h0 + hd] = (m + lg2(lsum)) * kLn2;
+          uint2 r;
+          r.x = E::pack(a.x * inv, a.y * inv);
+          r.y = E::pack(a.z * inv, a.w * inv);
+          *reinterpret_cast<uint2*>(static_cast<T*>(p.o) + (size_t(w.s) * p.H + h0 + hd) * D + dd) = r;
+          if (dd == 0) p.lse[size_t(w.s) * p.H + h0 + hd] = (m + lg2(lsum)) * kLn2;
         }
       }
-      fresh = true;
-      first = false;
+      if (ch + 1 < D / L::kJoinCols) named_bar_sync(1, 128);
     }
-    if (i + 1 < n_tiles) w.next(cum, p.S, p.units);
+    // the next copy into this stage follows the join's reads and writes there
+    fence_proxy_async_smem();
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&empty[st]);
+    fresh = true;
   }
 }
 
@@ -603,10 +623,10 @@ __global__ void __launch_bounds__(128) fa_decode_join_kernel(const DecodeParams 
   const int s = blockIdx.x / p.H, h = blockIdx.x % p.H;
   const int kvh = h / p.group, hg = h % p.group;
   const int unit = kvh * p.blocks + hg / (8 * NB), hd = hg % (8 * NB);
-  const int c0 = p.cum[s], nt = p.cum[s + 1] - c0, all = p.cum[p.S];
-  if (nt == 0) return;
+  const int c0 = p.cum[s], places = p.cum[s + 1] - c0, all = p.cum[p.S];
+  if (places == 0) return;
   const long long total = (long long)all * p.units;
-  const long long xa = (long long)c0 * p.units + (long long)unit * nt, xb = xa + nt;
+  const long long xa = (long long)c0 * p.units + (long long)unit * places, xb = xa + places - 1;
   const int ca = int(((xa + 1) * p.ctas - 1) / total), cb = int((xb * p.ctas - 1) / total);
   if (ca == cb) return;                     // a whole unit in one stretch
   const size_t slot = 8 * NB * (D + 2);
