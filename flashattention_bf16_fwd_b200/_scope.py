@@ -31,17 +31,23 @@ def call(fn, t, stream, *args):
 
 
 def same_device(t, *others):
+    at = t.get_device()
     for x in others:
-        if x is not None and x.device != t.device:
+        if x is not None and x.get_device() != at:
             raise ValueError("tensors must share one device")
 
 
-def int32(name, t, shape):
+def int32(name, t, *shape):
     """t: a contiguous int32 tensor of this shape (None: any length)."""
-    if t.dtype != torch.int32 or t.dim() != len(shape) or not t.is_contiguous() or any(
-            want is not None and have != want for have, want in zip(t.shape, shape)):
-        raise ValueError(f"{name} must be a contiguous int32 tensor of shape "
-                         f"[{', '.join('*' if n is None else str(n) for n in shape)}], got {t.dtype} {tuple(t.shape)}")
+    have = t.shape
+    if t.dtype is torch.int32 and len(have) == len(shape) and t.is_contiguous():
+        for n, want in zip(have, shape):
+            if n != want and want is not None:
+                break
+        else:
+            return
+    raise ValueError(f"{name} must be a contiguous int32 tensor of shape "
+                     f"[{', '.join('*' if n is None else str(n) for n in shape)}], got {t.dtype} {tuple(have)}")
 
 
 def count(n) -> int:

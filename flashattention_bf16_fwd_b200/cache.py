@@ -88,8 +88,8 @@ def _table(table, lens, S=None):
     shape = table.shape
     if not (len(shape) == 2 and lens.shape == shape[:1] and (S is None or S == shape[0]) and table.dtype is torch.int32
             and lens.dtype is torch.int32 and table.is_contiguous() and lens.is_contiguous()):
-        _scope.int32("table", table, (S, None))
-        _scope.int32("lens", lens, (table.shape[0],))
+        _scope.int32("table", table, S, None)
+        _scope.int32("lens", lens, table.shape[0])
     return shape
 
 
@@ -143,7 +143,7 @@ def cache_append(k, v, k_pages, v_pages, table, lens, cu=None, stream=None):
         raise ValueError(f"k and v must have one row per token ({S} sequences), got {T} and {v.shape[0]}")
     at = k_pages.get_device()
     if cu is not None:
-        _scope.int32("cu", cu, (S + 1,))
+        _scope.int32("cu", cu, S + 1)
         _scope.same_device(k_pages, cu)
     if not at == v_pages.get_device() == k.get_device() == v.get_device() == table.get_device() == lens.get_device():
         raise ValueError("tensors must share one device")
@@ -159,7 +159,7 @@ def cache_append(k, v, k_pages, v_pages, table, lens, cu=None, stream=None):
 def _page_tables(refs, table, lens, P=None):
     """(P, S, M) of a cache's tables."""
     if refs.dim() != 1 or refs.dtype is not torch.int32 or not refs.is_contiguous() or (P is not None and refs.shape[0] != P):
-        _scope.int32("refs", refs, (P,))
+        _scope.int32("refs", refs, P)
     S, M = _table(table, lens)
     if not refs.get_device() == table.get_device() == lens.get_device():
         raise ValueError("tensors must share one device")
@@ -171,7 +171,7 @@ def cache_reserve(refs, table, lens, add, page: int, stream=None):
     [1] on the device: 0 when done, the number of pages lacking (nothing is
     changed then), or -1 (a length or an entry of add is out of range)."""
     P, S, M = _page_tables(refs, table, lens)
-    _scope.int32("add", add, (S,))
+    _scope.int32("add", add, S)
     _scope.same_device(refs, add)
     return _scope.call(_reserve, refs, stream, refs, table, lens, add, (S, P, page, M))
 
@@ -192,8 +192,8 @@ def cache_fork(k_pages, v_pages, refs, table, lens, src, dst, stream=None, works
     L, P, Hkv, page, d = _pages(k_pages, v_pages, True)
     _elem(k_pages)
     _, S, M = _page_tables(refs, table, lens, P)
-    _scope.int32("src", src, (None,))
-    _scope.int32("dst", dst, (src.shape[0],))
+    _scope.int32("src", src, None)
+    _scope.int32("dst", dst, src.shape[0])
     _scope.same_device(refs, k_pages, v_pages, src, dst, workspace)
     return _scope.call(_fork, refs, stream, k_pages, v_pages, refs, table, lens, src, dst, workspace,
                        (src.shape[0], L, S, Hkv, d, P, page, M))
@@ -215,7 +215,7 @@ def cache_free(refs, table, lens, seqs, page: int, stream=None):
     """End the sequences ``seqs`` (int32 [F]): their pages' counts fall by 1,
     their table entries become -1 and their lengths 0."""
     P, S, M = _page_tables(refs, table, lens)
-    _scope.int32("seqs", seqs, (None,))
+    _scope.int32("seqs", seqs, None)
     _scope.same_device(refs, seqs)
     status = _scope.call(lib.fa_cache_free, refs, stream, refs.data_ptr(), table.data_ptr(), lens.data_ptr(),
                          seqs.data_ptr(), seqs.shape[0], S, P, page, M)

@@ -80,16 +80,56 @@ __global__ void __launch_bounds__(256) fa_bwd_dq_kernel(const float* __restrict_
   reinterpret_cast<uint4*>(dq)[i] = w;
 }
 
+// n / d for 0 <= n < 2^31 by a multiplication with ceil(2^(31 + s) / d), s =
+// ceil(log2 d), which fits 32 bits (Granlund and Montgomery, division by
+// invariant integers): n times its excess over 2^(31 + s) / d is below one part
+// of d, so the shifted product is exact.
+struct FastDiv {
+  uint32_t m, s;
+  FastDiv() = default;
+  explicit FastDiv(int d) : s(0) {
+    while ((1ll << s) < d) ++s;
+    m = uint32_t(((1ull << (31 + s)) + d - 1) / d);
+  }
+  __device__ __forceinline__ int div(int n) const { return int((uint64_t(uint32_t(n)) * m) >> (31 + s)); }
+};
+
+// How the windowed backward cuts its work.  A key tile is seen by `near` query
+// tiles, from its own on; one that holds sinks is also seen by every later query
+// tile, its far part.  Over the group of query heads that is near * group steps,
+// and (n_q - near - tile) * group; either is cut into parts of about the same
+// number of steps, which the host chooses.
+struct BwdPieces {
+  int n_q, near, group;
+  int near_parts;       // parts of a key tile's window steps
+  int split, far_parts; // key tiles with a far part; its parts
+  int far_rows;         // sink rows in them
+  bool gaps;            // some parts are empty
+  FastDiv by_heads, by_tiles, by_near, by_far;   // by BH, n_q, near_parts, far_parts
+  // query tiles of key tile kv's window (far = false) or of its far part
+  __host__ __device__ __forceinline__ int tiles(bool far, int kv) const {
+    const int left = n_q - kv;
+    return far ? left - near : left < near ? left : near;
+  }
+  // Part c has the steps from c * (steps / parts) + min(c, steps % parts) on: none
+  // where there are fewer steps than parts and c is not below them.
+  __host__ __device__ __forceinline__ int filled(bool far, int kv) const {     // parts that are not empty
+    const int steps = tiles(far, kv) * group, parts = far ? far_parts : near_parts;
+    return steps < parts ? steps : parts;
+  }
+};
+
 // The windowed backward's last launch: dQ = scale * accumulator as above (the
-// first `dq_blocks` blocks), and the sink rows of split key tiles as the sum of
-// their pieces, in order (one thread per row, dK or dV, and four columns).
-// part: [BH][pieces][rows][dK, dV][d]; dk, dv: [BH][N][d].
+// first `dq_blocks` blocks), and the rows of dK and dV that were left in parts,
+// summed in the parts' order (one thread per row, dK or dV, and four columns):
+// every row where near_parts > 1, else the sink rows of tiles with a far part.
 template <typename E>
 __global__ void __launch_bounds__(256)
     fa_bwd_window_finish_kernel(const float* __restrict__ acc, typename E::T* __restrict__ dq, float scale,
-                                long long n8, unsigned dq_blocks, const float* __restrict__ part,
-                                typename E::T* __restrict__ dk, typename E::T* __restrict__ dv, int pieces, int rows,
-                                int N, int d, long long part_items) {
+                                long long n8, unsigned dq_blocks, const float* __restrict__ near_part,
+                                const float* __restrict__ far_part, typename E::T* __restrict__ dk,
+                                typename E::T* __restrict__ dv, const BwdPieces pc, int rows, int N, int d,
+                                long long part_items) {
   grid_dep_wait();
   grid_dep_launch();
   if (blockIdx.x < dq_blocks) {
@@ -108,21 +148,30 @@ __global__ void __launch_bounds__(256)
   const long long i = (long long)(blockIdx.x - dq_blocks) * blockDim.x + threadIdx.x;
   if (i >= part_items) return;
   const int per_row = d / 2;                             // dK and dV, four columns each
-  const int c = int(i % per_row);
-  const long long row = i / per_row;                     // (head, key)
-  const long long bh = row / rows;
-  const int key = int(row % rows);
-  const float* x = part + (bh * pieces * rows + key) * 2 * d + 4 * c;
+  const int c4 = int(i % per_row) * 4;
+  const long long bh = i / per_row / rows;
+  const int key = int(i / per_row % rows), kv = key >> 7;
   float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
-  for (int s = 0; s < pieces; ++s) {
-    const float4 b = *reinterpret_cast<const float4*>(x + (long long)s * rows * 2 * d);
+  auto add = [&](const float* x) {
+    const float4 b = *reinterpret_cast<const float4*>(x + c4);
     a.x += b.x;
     a.y += b.y;
     a.z += b.z;
     a.w += b.w;
+  };
+  if (pc.near_parts > 1) {
+    const int n = pc.filled(false, kv);
+#pragma unroll 8
+    for (int c = 0; c < n; ++c) add(near_part + ((bh * pc.near_parts + c) * N + key) * 2 * d);
   }
-  const bool is_v = 4 * c >= d;
-  typename E::T* out = (is_v ? dv : dk) + (bh * N + key) * d + (4 * c - (is_v ? d : 0));
+  if (key < pc.far_rows) {
+    const int n = pc.filled(true, kv);                   // slot 0: the window's own sum
+#pragma unroll 8
+    for (int c = pc.near_parts > 1 ? 1 : 0; c <= n; ++c)
+      add(far_part + ((bh * (1 + pc.far_parts) + c) * pc.far_rows + key) * 2 * d);
+  }
+  const bool is_v = c4 >= d;
+  typename E::T* out = (is_v ? dv : dk) + (bh * N + key) * d + (c4 - (is_v ? d : 0));
   *reinterpret_cast<uint2*>(out) = make_uint2(E::pack(a.x, a.y), E::pack(a.z, a.w));
 }
 
@@ -137,12 +186,15 @@ struct BwdParams {
   int H, group;         // query heads per batch entry; query heads per K/V head (1 = no sharing)
   float scale, scale_log2;
   int after_pre;        // 1: launched right after fa_bwd_pre_kernel on the same stream
-  // windowed kernel (BwdWindow)
+};
+
+// The windowed kernel's.  (A type of its own: with these fields in BwdParams the
+// other kernels' arguments pass 1 KB, and their launches take 1 us longer.)
+struct BwdWindowParams : BwdParams {
   int window, sinks;    // key j is visible where j <= i and (i - j < window or j < sinks)
-  int near;             // query tiles whose window reaches a key tile
-  int split, chunks, chunk;   // key tiles with a far part; its pieces, and their query tiles
-  float* part;          // [BH][1 + chunks][part_rows][dK, dV][D]: pieces of the split tiles' sink rows
-  int part_rows;
+  BwdPieces pc;
+  float* near_part;     // [BH][near_parts][N][dK, dV][D], where near_parts > 1
+  float* far_part;      // [BH][1 + far_parts][far_rows][dK, dV][D], where there are far parts
 };
 
 template <int D>
@@ -197,12 +249,19 @@ struct BwdLayout {
 // shares the K/V head (dK, dV accumulate over all of them): n_it steps.
 struct BwdItem {
   int bh, kv_tile, key0, i_start, n_it_head, n_it;
-  int piece;            // windowed kernel: -1, or which piece of a split key tile (0: its window)
+};
+
+// The windowed kernel's: its first step, and where dK and dV go.  (A type of its
+// own: these fields in BwdItem cost the other kernels registers, a spill at d = 128.)
+struct BwdWindowItem : BwdItem {
+  int step0;
+  float* part;          // FP32 [rows][dK, dV][D] of the rows below part_rows, or nullptr
+  int part_rows;
+  bool direct;          // the other rows are final: to dK and dV
 };
 
 __device__ __forceinline__ BwdItem bwd_item_at(const BwdParams& p, int bh, int kv_tile) {
   BwdItem w;
-  w.piece = -1;
   w.bh = bh;
   w.kv_tile = kv_tile;
   w.key0 = kv_tile * 128;
@@ -254,47 +313,85 @@ struct BwdSched {
   }
 };
 
-// The windowed kernel's items.  A key tile is seen by `near` query tiles, from
-// its own on; one that holds sinks is seen by every later query tile too.  As
-// one item it would take N / 128 steps where the others take `near`, and the
-// CTAs that drew such an item would finish long after the rest (H = 32 over
-// Hkv = 8, N = 8192, window 1024: 256 steps against 135 on average).  So the far
-// part is cut into pieces of `chunk` query tiles, items of their own, which
-// leave FP32 dK and dV of the sink rows; fa_bwd_window_finish_kernel adds the
-// pieces in a fixed order.  The far pieces come first, then the key tiles, head
-// by head: neighbours share their queries in the L2.
+// The windowed kernel's items: the parts of BwdPieces.  A tile with sinks as one
+// item would take N / 128 steps where the others take `near`, and few heads with
+// a wide window give fewer items than SMs; so both are cut, into items of about
+// the same length (every CTA takes as many), four steps at least (H = 4 over one
+// K/V head, N = 2048, d = 128, window 1024: 107 us uncut, 36 us).  Parts leave
+// FP32 dK and dV, which fa_bwd_window_finish_kernel adds in a fixed order; a
+// window in one part writes its final rows itself.  The far parts come first,
+// then the key tiles, head by head: neighbours share their queries in the L2.
+template <int D>
 struct BwdWindow {
   int rnd, item, n_far, n_items;
-  __device__ __forceinline__ explicit BwdWindow(const BwdParams& p) : rnd(0), item(snake_item(0)) {
-    n_far = p.split * p.chunks * p.BH;
-    n_items = n_far + p.n_kv * p.BH;
+  __device__ __forceinline__ explicit BwdWindow(const BwdWindowParams& p) : rnd(0), item(snake_item(0)) {
+    n_far = p.pc.split * p.pc.far_parts * p.BH;
+    n_items = n_far + p.n_kv * p.pc.near_parts * p.BH;
+    skip(p);
   }
   __device__ __forceinline__ bool valid() const { return item < n_items; }
-  __device__ __forceinline__ BwdItem get(const BwdParams& p) const {
-    BwdItem w;
-    const int n_q = p.n_kv;
-    int end;
-    if (item < n_far) {
-      const int c = item / p.BH % p.chunks;
-      w.bh = item % p.BH;
-      w.kv_tile = item / p.BH / p.chunks;
-      w.piece = 1 + c;
-      w.i_start = max(w.kv_tile + p.near, p.near + c * p.chunk);
-      end = min(n_q, p.near + (c + 1) * p.chunk);
+  // The roles of a CTA come here once per item, some between two MMAs: with
+  // plain divisions the backward of N=8192 d=64 window 1024 takes 600 us, with
+  // these 550.
+  __device__ __forceinline__ void where(const BwdWindowParams& p, bool& far, int& bh, int& kv, int& c) const {
+    far = item < n_far;
+    if (far) {
+      const int i = p.pc.by_heads.div(item);
+      bh = item - i * p.BH;
+      kv = p.pc.by_far.div(i);
+      c = i - kv * p.pc.far_parts;
     } else {
-      const int i = item - n_far;
-      w.bh = i / p.n_kv;
-      w.kv_tile = i % p.n_kv;
-      w.piece = w.kv_tile < p.split ? 0 : -1;
-      w.i_start = w.kv_tile;
-      end = min(n_q, w.kv_tile + p.near);
+      const int n = item - n_far, i = p.pc.by_near.div(n);
+      c = n - i * p.pc.near_parts;
+      bh = p.pc.by_tiles.div(i);
+      kv = i - bh * p.n_kv;
     }
+  }
+  // a tile with fewer steps than parts has empty ones
+  __device__ __forceinline__ void skip(const BwdWindowParams& p) {
+    if (!p.pc.gaps) return;
+    bool far;
+    int bh, kv, c;
+    while (valid()) {
+      where(p, far, bh, kv, c);
+      if (c < p.pc.filled(far, kv)) return;
+      item = snake_item(++rnd);
+    }
+  }
+  __device__ __forceinline__ void next(const BwdWindowParams& p) {
+    item = snake_item(++rnd);
+    skip(p);
+  }
+  __device__ __forceinline__ BwdWindowItem get(const BwdWindowParams& p) const {
+    BwdWindowItem w;
+    bool far;
+    int c;
+    where(p, far, w.bh, w.kv_tile, c);
     w.key0 = w.kv_tile * 128;
-    w.n_it_head = end - w.i_start;
+    w.i_start = w.kv_tile + (far ? p.pc.near : 0);
+    w.n_it_head = p.pc.tiles(far, w.kv_tile);
     w.n_it = w.n_it_head * p.group;
+    w.step0 = 0;
+    const int parts = far ? p.pc.far_parts : p.pc.near_parts;
+    if (parts > 1) {
+      const int per = (far ? p.pc.by_far : p.pc.by_near).div(w.n_it), more = w.n_it - per * parts;
+      w.step0 = c * per + min(c, more);
+      w.n_it = per + (c < more ? 1 : 0);
+    }
+    w.part = nullptr;
+    w.part_rows = 0;
+    w.direct = !far;
+    const long long bh = w.bh;
+    if (far || (p.pc.near_parts == 1 && w.kv_tile < p.pc.split)) {
+      w.part_rows = p.pc.far_rows;
+      w.part = p.far_part + (bh * (1 + p.pc.far_parts) + (far ? 1 + c : 0)) * p.pc.far_rows * (2 * D);
+    } else if (p.pc.near_parts > 1) {
+      w.part_rows = p.N;
+      w.part = p.near_part + (bh * p.pc.near_parts + c) * p.N * (2 * D);
+      w.direct = false;
+    }
     return w;
   }
-  __device__ __forceinline__ void next(const BwdParams&) { item = snake_item(++rnd); }
 };
 
 // The steps of an item in order: query tile qt of batch*query-head bh_q,
@@ -307,6 +404,10 @@ struct BwdSteps {
     q_end = w.i_start + w.n_it_head;
     qt = q_first;
     bh_q = (w.bh / hkv) * p.H + (w.bh % hkv) * p.group;
+  }
+  __device__ __forceinline__ void skip(int steps) {
+    for (; steps >= q_end - q_first; steps -= q_end - q_first) ++bh_q;
+    qt += steps;
   }
   __device__ __forceinline__ void next() {
     if (++qt == q_end) {
@@ -341,9 +442,10 @@ __global__ void __launch_bounds__(512, 1)
     fa_bwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
                   const __grid_constant__ CUtensorMap tm_v, const __grid_constant__ CUtensorMap tm_do,
                   const __grid_constant__ CUtensorMap tm_dq, const __grid_constant__ CUtensorMap tm_dk,
-                  const __grid_constant__ CUtensorMap tm_dv, const BwdParams p) {
+                  const __grid_constant__ CUtensorMap tm_dv,
+                  const std::conditional_t<kWin, BwdWindowParams, BwdParams> p) {
   using L = BwdLayout<D>;
-  using Sched = std::conditional_t<kWin, BwdWindow, BwdSched<kPairs>>;
+  using Sched = std::conditional_t<kWin, BwdWindow<D>, BwdSched<kPairs>>;
   extern __shared__ __align__(1024) uint8_t smem[];
   uint64_t* bars = reinterpret_cast<uint64_t*>(smem + L::kBarOff);
   uint64_t* kv_full = bars;        // [2]
@@ -436,7 +538,7 @@ __global__ void __launch_bounds__(512, 1)
       bool ok = true;
       bool dep_done = false;
       for (Sched sc(p); ok && sc.valid(); sc.next(p), ++n_done) {
-        const BwdItem w = sc.get(p);
+        const auto w = sc.get(p);
         const uint32_t ks = n_done % L::kKVStages;
         ok = __all_sync(0xffffffffu, mbar_wait(&kv_empty[ks], ((n_done / L::kKVStages) & 1) ^ 1, wd));
         if (!ok) break;
@@ -449,6 +551,7 @@ __global__ void __launch_bounds__(512, 1)
           }
         }
         BwdSteps sp(p, w);
+        if constexpr (kWin) sp.skip(w.step0);
         for (int it = 0; it < w.n_it; ++it, ++g, sp.next()) {
           const uint32_t st = g % L::kQStages;
           const int q0 = sp.qt * 128;
@@ -486,8 +589,9 @@ __global__ void __launch_bounds__(512, 1)
       uint32_t g = 0;
       bool ok = true;
       for (Sched sc(p); ok && sc.valid(); sc.next(p)) {
-        const BwdItem w = sc.get(p);
+        const auto w = sc.get(p);
         BwdSteps sp(p, w);
+        if constexpr (kWin) sp.skip(w.step0);
         for (int it = 0; it < w.n_it; ++it, ++g, sp.next()) {
           const int q0 = sp.qt * 128;
           // dO_i: with a single buffer it is refilled once dV_{i-1} has read it
@@ -552,7 +656,7 @@ __global__ void __launch_bounds__(512, 1)
         // the compute warps do not wait for them at the item boundary
         bool first_issued = false;
         for (Sched sc(p); ok && sc.valid(); sc.next(p), ++n_done) {
-          const BwdItem w = sc.get(p);
+          const auto w = sc.get(p);
           const uint32_t ks = n_done % L::kKVStages;
           const uint32_t sk = k_of(n_done);
           const uint32_t sv = sk + (L::kTileBytes >> 4);
@@ -656,9 +760,10 @@ __global__ void __launch_bounds__(512, 1)
     uint32_t g = 0;
     bool ok = true;
     for (Sched sc(p); ok && sc.valid(); sc.next(p)) {
-      const BwdItem w = sc.get(p);
+      const auto w = sc.get(p);
       const bool key_in = w.key0 + kr < p.N;
       BwdSteps sp(p, w);
+      if constexpr (kWin) sp.skip(w.step0);
       for (int it = 0; it < w.n_it; ++it, ++g, sp.next()) {
         const uint32_t st = g % L::kQStages;
         const int qt = sp.qt;
@@ -855,8 +960,9 @@ __global__ void __launch_bounds__(512, 1)
     uint32_t n_done = 0;
     bool ok = true;
     for (Sched sc(p); ok && sc.valid(); sc.next(p), ++n_done) {
-      const BwdItem w = sc.get(p);
+      const auto w = sc.get(p);
       BwdSteps sp(p, w);
+      if constexpr (kWin) sp.skip(w.step0);
       for (int it = 0; it < w.n_it; ++it, ++g, sp.next()) {
         ok = __all_sync(0xffffffffu, mbar_wait(dq_full, g & 1, wd));
         if (!ok) break;
@@ -901,44 +1007,47 @@ __global__ void __launch_bounds__(512, 1)
       if (!ok) break;
       tc_fence_after();
       const int key = w.key0 + rr;
-      if (kWin && w.piece >= 0) {
-        // a piece of a split key tile: FP32 sums of the sink rows; the other rows
-        // are seen by the window alone and are final
-        const bool sink = key < p.part_rows;
-        float* part = p.part + ((size_t(w.bh) * (1 + p.chunks) + w.piece) * p.part_rows + key) * (2 * D);
-        for (int which = 0; which < 2; ++which) {
-          const uint32_t t_src = tmem + lane_base + (which ? L::kTmDK : L::kTmDV);
-          const float mul = which ? p.scale : 1.f;
-          uint4* dst = reinterpret_cast<uint4*>(static_cast<typename E::T*>(which ? p.dk : p.dv) +
-                                                (size_t(w.bh) * p.N + key) * D);
-          float4* dstf = reinterpret_cast<float4*>(part + (which ? 0 : D));
+      bool in_parts = false;
+      if constexpr (kWin) in_parts = w.part != nullptr;
+      if (in_parts) {
+        if constexpr (kWin) {
+          // a part of a key tile: FP32 sums of its rows, the others as usual
+          const bool sum = key < w.part_rows;
+          float* part = w.part + size_t(key) * (2 * D);
+          for (int which = 0; which < 2; ++which) {
+            const uint32_t t_src = tmem + lane_base + (which ? L::kTmDK : L::kTmDV);
+            const float mul = which ? p.scale : 1.f;
+            uint4* dst = reinterpret_cast<uint4*>(static_cast<typename E::T*>(which ? p.dk : p.dv) +
+                                                  (size_t(w.bh) * p.N + key) * D);
+            float4* dstf = reinterpret_cast<float4*>(part + (which ? 0 : D));
 #pragma unroll 1
-          for (int c = 0; c < D / 32; ++c) {
-            uint32_t r[32];
-            tmem_ld32(t_src + c * 32, r);
-            tmem_ld_wait(r);
+            for (int c = 0; c < D / 32; ++c) {
+              uint32_t r[32];
+              tmem_ld32(t_src + c * 32, r);
+              tmem_ld_wait(r);
 #pragma unroll
-            for (int i = 0; i < 32; ++i) r[i] = __float_as_uint(__uint_as_float(r[i]) * mul);
-            if (sink) {
+              for (int i = 0; i < 32; ++i) r[i] = __float_as_uint(__uint_as_float(r[i]) * mul);
+              if (sum) {
 #pragma unroll
-              for (int i = 0; i < 8; ++i)
-                dstf[c * 8 + i] = make_float4(__uint_as_float(r[4 * i]), __uint_as_float(r[4 * i + 1]),
-                                              __uint_as_float(r[4 * i + 2]), __uint_as_float(r[4 * i + 3]));
-            } else if (w.piece == 0 && key < p.N) {
+                for (int i = 0; i < 8; ++i)
+                  dstf[c * 8 + i] = make_float4(__uint_as_float(r[4 * i]), __uint_as_float(r[4 * i + 1]),
+                                                __uint_as_float(r[4 * i + 2]), __uint_as_float(r[4 * i + 3]));
+              } else if (w.direct && key < p.N) {
 #pragma unroll
-              for (int i = 0; i < 4; ++i) {
-                uint4 v;
-                v.x = E::pack(__uint_as_float(r[8 * i]), __uint_as_float(r[8 * i + 1]));
-                v.y = E::pack(__uint_as_float(r[8 * i + 2]), __uint_as_float(r[8 * i + 3]));
-                v.z = E::pack(__uint_as_float(r[8 * i + 4]), __uint_as_float(r[8 * i + 5]));
-                v.w = E::pack(__uint_as_float(r[8 * i + 6]), __uint_as_float(r[8 * i + 7]));
-                dst[c * 4 + i] = v;
+                for (int i = 0; i < 4; ++i) {
+                  uint4 v;
+                  v.x = E::pack(__uint_as_float(r[8 * i]), __uint_as_float(r[8 * i + 1]));
+                  v.y = E::pack(__uint_as_float(r[8 * i + 2]), __uint_as_float(r[8 * i + 3]));
+                  v.z = E::pack(__uint_as_float(r[8 * i + 4]), __uint_as_float(r[8 * i + 5]));
+                  v.w = E::pack(__uint_as_float(r[8 * i + 6]), __uint_as_float(r[8 * i + 7]));
+                  dst[c * 4 + i] = v;
+                }
               }
             }
           }
+          tc_fence_before();
+          mbar_arrive(dkv_free);                       // the next item may overwrite dK, dV
         }
-        tc_fence_before();
-        mbar_arrive(dkv_free);                       // the next item may overwrite dK, dV
       } else if constexpr (D == 64) {
         // dV and dK through this warp's two staging boxes (32 rows each, the
         // 128-byte swizzle) and one TMA store box each; rows past N are

@@ -56,32 +56,50 @@ int check_window(int B, int H, int Hkv, int N, int d, int window, int sinks, flo
   return window >= 1 && sinks >= 0 ? FA_OK : FA_ERR_WINDOW;
 }
 
-// How the backward divides the key tiles (BwdWindow), and where its workspace
-// keeps what.
+// How the backward cuts its work (BwdPieces), and where its workspace keeps what.
+// It goes by the sizes alone, so that the sums do not depend on the device.
 struct BwdPlan {
-  int window, sinks, near, split, chunks, chunk, part_rows;
-  size_t dsum, part, bytes;   // offsets; the dQ accumulator is at 0
+  int window, sinks;
+  BwdPieces pc;
+  long long n_items;
+  size_t dsum, near, far, bytes;   // offsets; the dQ accumulator is at 0
 };
 
 BwdPlan bwd_plan(int B, int H, int Hkv, int N, int d, int window, int sinks) {
   BwdPlan w{};
   w.window = window < N ? window : N;
   w.sinks = sinks < N ? sinks : N;
-  const int n_q = (N + 127) / 128;
-  w.near = (126 + w.window) / 128 + 1;
-  if (w.near > n_q) w.near = n_q;
-  const int far = n_q - w.near, sink_tiles = (w.sinks + 127) / 128;
-  w.split = sink_tiles < far ? sink_tiles : far;
-  // as many steps as a window has, and enough that K, V and the pieces are worth
-  // their loads; at least one per sink tile, so that no piece is empty
-  w.chunk = w.near > 8 ? w.near : 8;
-  if (w.chunk < sink_tiles) w.chunk = sink_tiles;
-  w.chunks = w.split ? (far + w.chunk - 1) / w.chunk : 0;
-  w.part_rows = w.sinks < 128 * w.split ? w.sinks : 128 * w.split;
-  const size_t rows = size_t(B) * H * N;
+  BwdPieces& pc = w.pc;
+  pc.n_q = (N + 127) / 128;
+  pc.near = (126 + w.window) / 128 + 1;
+  if (pc.near > pc.n_q) pc.near = pc.n_q;
+  pc.group = H / Hkv;
+  const int far = pc.n_q - pc.near, sink_tiles = (w.sinks + 127) / 128;
+  pc.split = sink_tiles < far ? sink_tiles : far;
+  pc.far_rows = w.sinks < 128 * pc.split ? w.sinks : 128 * pc.split;
+  // steps of all items; a third of a CTA's share of them, four at least (an item
+  // loads K and V and writes its sums, about two steps' time)
+  const long long BHkv = (long long)B * Hkv;
+  const long long near_steps = (long long)pc.n_q * pc.near - (long long)pc.near * (pc.near - 1) / 2;
+  const long long far_steps = (long long)pc.split * far - (long long)pc.split * (pc.split - 1) / 2;
+  const long long share = ((near_steps + far_steps) * BHkv * pc.group + 3 * 148 - 1) / (3 * 148);
+  const long long item = share > 4 ? share : 4;
+  pc.near_parts = int(((long long)pc.near * pc.group + item - 1) / item);
+  // far parts about as long as the others: every CTA takes as many items
+  const int part = pc.near * pc.group / pc.near_parts, far_item = part > 4 ? part : 4;
+  const long long far_len = (long long)far * pc.group;
+  pc.far_parts = !pc.split ? 0 : far_len < far_item ? 1 : int((far_len + far_item / 2) / far_item);
+  pc.gaps = pc.near_parts > pc.group || (pc.split && pc.far_parts > (far - pc.split + 1) * pc.group);
+  pc.by_heads = FastDiv(int(BHkv));
+  pc.by_tiles = FastDiv(pc.n_q);
+  pc.by_near = FastDiv(pc.near_parts);
+  pc.by_far = FastDiv(pc.far_parts ? pc.far_parts : 1);
+  w.n_items = BHkv * ((long long)pc.n_q * pc.near_parts + (long long)pc.split * pc.far_parts);
+  const size_t rows = size_t(B) * H * N, row = size_t(2) * d * sizeof(float);
   w.dsum = align256(rows * d * sizeof(float));
-  w.part = w.dsum + align256(rows * sizeof(float));
-  w.bytes = w.part + (w.split ? align256(size_t(B) * Hkv * (1 + w.chunks) * w.part_rows * 2 * d * sizeof(float)) : 0);
+  w.near = w.dsum + align256(rows * sizeof(float));
+  w.far = w.near + (pc.near_parts > 1 ? align256(size_t(BHkv) * pc.near_parts * N * row) : 0);
+  w.bytes = w.far + (pc.split ? align256(size_t(BHkv) * (1 + pc.far_parts) * pc.far_rows * row) : 0);
   return w;
 }
 
@@ -131,12 +149,13 @@ int window_bwd(const void* q, const void* k, const void* v, const void* o, const
     return FA_ERR_DEVICE;
   float* dq_acc = reinterpret_cast<float*>(workspace);
   float* dsum = reinterpret_cast<float*>(workspace + w.dsum);
-  float* part = reinterpret_cast<float*>(workspace + w.part);
+  float* near_part = reinterpret_cast<float*>(workspace + w.near);
+  float* far_part = reinterpret_cast<float*>(workspace + w.far);
   const long long rows = (long long)BH * N;
   if (launch(fa_bwd_pre_kernel<E>, dim3(unsigned((rows * 8 + 255) / 256)), dim3(256), 0, stream,
              static_cast<const T*>(o), static_cast<const T*>(dout), dsum, dq_acc, rows, D) != cudaSuccess)
     return FA_ERR_LAUNCH;
-  BwdParams p{};
+  BwdWindowParams p{};
   p.lse = lse;
   p.dsum = dsum;
   p.dq_acc = dq_acc;
@@ -154,23 +173,20 @@ int window_bwd(const void* q, const void* k, const void* v, const void* o, const
   p.after_pre = 1;
   p.window = w.window;
   p.sinks = w.sinks;
-  p.near = w.near;
-  p.split = w.split;
-  p.chunks = w.chunks;
-  p.chunk = w.chunk;
-  p.part = part;
-  p.part_rows = w.part_rows;
-  const long long n_items = (long long)BHkv * (p.n_kv + w.split * w.chunks);
-  if (launch(fa_bwd_kernel<D, E, false, true>, dim3(unsigned(n_items < num_sms ? n_items : num_sms)),
+  p.pc = w.pc;
+  p.near_part = near_part;
+  p.far_part = far_part;
+  if (launch(fa_bwd_kernel<D, E, false, true>, dim3(unsigned(w.n_items < num_sms ? w.n_items : num_sms)),
              dim3(L::kThreads), L::kAlloc, stream, mq, mk, mv, mdo, mdq, mdk, mdv, p) != cudaSuccess)
     return FA_ERR_LAUNCH;
   const long long n8 = rows * D / 8;
   const unsigned dq_blocks = unsigned((n8 + 255) / 256);
-  const long long part_items = w.split ? (long long)BHkv * w.part_rows * (D / 2) : 0;
+  const int part_rows = w.pc.near_parts > 1 ? N : w.pc.far_rows;
+  const long long part_items = (long long)BHkv * part_rows * (D / 2);
   if (launch(fa_bwd_window_finish_kernel<E>, dim3(dq_blocks + unsigned((part_items + 255) / 256)), dim3(256), 0,
              stream, static_cast<const float*>(dq_acc), static_cast<T*>(dq), scale, n8, dq_blocks,
-             static_cast<const float*>(part), static_cast<T*>(dk), static_cast<T*>(dv), 1 + w.chunks, w.part_rows, N,
-             D, part_items) != cudaSuccess)
+             static_cast<const float*>(near_part), static_cast<const float*>(far_part), static_cast<T*>(dk),
+             static_cast<T*>(dv), w.pc, part_rows, N, D, part_items) != cudaSuccess)
     return FA_ERR_LAUNCH;
   return FA_OK;
 }

@@ -72,6 +72,9 @@ CASES = [  # B, H, Hkv, N, d, window, sinks, type
     (1, 3, 1, 2100, 64, 200, 4, "bf16"),
     (1, 2, 1, 1900, 128, 90, 3, "fp16"),
     (1, 2, 2, 1500, 64, 2, 129, "bf16"),
+    (1, 8, 1, 700, 64, 300, 4, "bf16"),          # windows and far parts cut, some parts empty
+    (1, 4, 1, 2500, 128, 600, 140, "bf16"),
+    (1, 5, 1, 1300, 64, 400, 0, "fp16"),
 ]
 
 

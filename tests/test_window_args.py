@@ -80,12 +80,16 @@ def test_arguments(win, name, args):
 def test_workspace_size(win):
     size = win.fa_window_bwd_workspace_size
     up = lambda x: -(-x // 256) * 256
-    rows = 2 * 4 * 1000
+    rows = 8 * 12 * 1024
     base = up(rows * 64 * 4) + up(rows * 4)
-    assert size(2, 4, 2, 1000, 64, 64, 0) == base
-    assert size(2, 4, 2, 1000, 64, 5000, 4) == base            # no query is past the window
-    # 8 query tiles, 2 in a window, 6 behind it: one piece beside the window's
-    assert size(2, 4, 2, 1000, 64, 64, 4) == base + up(2 * 2 * 2 * 4 * 2 * 64 * 4)
+    assert size(8, 12, 12, 1024, 64, 256, 0) == base
+    assert size(8, 12, 12, 1024, 64, 5000, 4) == base          # no query is past the window
+    # 8 query tiles, 3 in a window, 5 behind it in one part beside the window's
+    assert size(8, 12, 12, 1024, 64, 256, 4) == base + up(96 * 2 * 4 * 2 * 64 * 4)
+    # one head: its 3 tiles of 3, 2 and 1 steps fit the least length of a part
+    assert size(1, 1, 1, 300, 64, 256, 0) == up(300 * 64 * 4) + up(300 * 4)
+    # four heads over one: 12 steps a tile, in three parts of all rows
+    assert size(1, 4, 1, 300, 64, 256, 0) == up(1200 * 64 * 4) + up(1200 * 4) + up(3 * 300 * 2 * 64 * 4)
     assert size(2, 4, 2, 1000, 64, 0, 4) == 0
     assert size(2, 4, 3, 1000, 64, 64, 4) == 0
     assert size(1, 1, 1, 1 << 20, 64, 10**12, 10**12) == size(1, 1, 1, 1 << 20, 64, 1 << 20, 1 << 20)
