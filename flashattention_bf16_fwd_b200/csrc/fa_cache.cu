@@ -198,8 +198,7 @@ int fa_cache_append(const void* k, const void* v, void* k_pages, void* v_pages, 
   a.k_stride = k_stride / 8;
   a.v_stride = v_stride / 8;
   a.T = T;
-  const int blocks = T / 8 + (T % 8 != 0), most = 8 * num_sms;
-  return launch(fa_cache_append_kernel, dim3(blocks < most ? blocks : most), dim3(256), 0,
+  return launch(fa_cache_append_kernel, dim3(T / 8 + (T % 8 != 0)), dim3(256), 0,
                 static_cast<cudaStream_t>(stream), a) == cudaSuccess
              ? FA_OK
              : FA_ERR_LAUNCH;
