@@ -122,10 +122,12 @@ int fa_decode(const void* q, const void* k_pages, const void* v_pages, const int
   int rc = check_cache(S, Hkv, d, P, page, M);
   if (rc != FA_OK) return rc;
   if (H < Hkv || H % Hkv || (long long)S * H * d >= (1ll << 31)) return FA_ERR_SHAPE;
-  // tiles of the whole batch, counted in 64 bits; those of one sequence in 32
   if (q_stride < (long long)H * d || q_stride % 8 || q_stride >= (1ll << 31) || window < 0 || sinks < 0 ||
       (window == 0 && sinks != 0))
     return FA_ERR_CACHE_SHAPE;
+  // the kernel counts the tiles of one sequence, over all its heads, and of one CTA in 32 bits
+  const long long tiles = ((long long)M * page / 64 + 2) * H;
+  if (tiles >= (1ll << 31) || tiles * S >= (1ll << 38)) return FA_ERR_CACHE_SHAPE;
   if (!std::isfinite(scale) || !(scale > 0.f) || (elem != FA_ELEM_BF16 && elem != FA_ELEM_F16)) return FA_ERR_ARG;
   if (!aligned16(q) || !aligned16(k_pages) || !aligned16(v_pages) || !aligned16(o) || !aligned4(table) ||
       !aligned4(lens) || !aligned4(lse))
@@ -160,7 +162,8 @@ int fa_decode(const void* q, const void* k_pages, const void* v_pages, const int
   prm.window = window;
   prm.sinks = sinks;
   // two CTAs per SM, or one per place where there are fewer
-  const long long most = (long long)S * prm.units * (((long long)M * page + tile - 1) / tile + 1);
+  const long long places = ((long long)M * page + tile - 1) / tile + 1;      // of a unit, at most
+  const long long most = (long long)S * prm.units * places;
   const int two = 2 * num_sms < kDecMaxCtas ? 2 * num_sms : kDecMaxCtas;
   prm.ctas = int(most < two ? most : two);
   prm.scale_log2 = float(double(scale) * 1.4426950408889634);

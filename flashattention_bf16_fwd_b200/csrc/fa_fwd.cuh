@@ -640,8 +640,10 @@ __global__ void __launch_bounds__(384, 1)
           // repetitions.  P scaled by a power of two is rounded alike in bf16; in
           // fp16 the headroom is smaller, for P below 2^-14 loses bits there.
           // N = 16384, window 4096, d = 128: 1186 us with the exact shift,
-          // 936 us with headroom.  (A share of the exponentials as a polynomial on
-          // the FMA pipe: 893 us for 1/8 of them, 954 for 1/4, against 864 for none.)
+          // 936 us with headroom.  (What gained nothing, against 864: a share of the
+          // exponentials as a polynomial on the FMA pipe, 893 us for 1/8 of them, 954
+          // for 1/4; four softmax warpgroups, two threads to a row that exchange their
+          // maxima, 1063.)
           constexpr float kHeadroom = E::kMmaFmt == 1 ? 8.f : 4.f;
           auto tile = [&](auto edge) {
             // A tile in which some row of the warp does not see every key is taken

@@ -64,6 +64,7 @@ extern "C" {
  * both are reported.
  * Equal lens, shapes and inputs give equal bits; the split of the work, and so
  * the order of the sums, depends on the lengths of the whole batch.
+ * H*M*page/64 below 2^31, S*H*M*page/64 below 2^38 (FA_ERR_CACHE_SHAPE).
  *   workspace : device scratch of fa_decode_workspace_size() bytes, used from
  *       the call until its kernels have run: calls that may run at the same
  *       time need one each.

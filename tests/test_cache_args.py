@@ -103,6 +103,7 @@ def test_decode_arguments(fa):
     dec = lambda **kw: call(fa, "fa_decode", DECODE, **kw)
     assert dec(H=9) == SHAPE
     assert dec(H=1) == SHAPE
+    assert dec(S=1, M=1 << 26, H=128, Hkv=2, q_stride=128 * 64) == CSHAPE       # 2^31 tiles over one sequence's heads
     for kw in (dict(q_stride=504), dict(q_stride=516), dict(window=-1), dict(window=4, sinks=-1), dict(sinks=3)):
         assert dec(**kw) == CSHAPE, kw
     for kw in (dict(scale=0.0), dict(scale=float("nan")), dict(scale=-1.0), dict(elem=2), dict(elem=-1)):

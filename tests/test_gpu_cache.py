@@ -427,3 +427,30 @@ def test_decoding_step_in_a_graph(fa):
             flat = [torch.stack([x[j] for x in c["seen"]], 2) for j in range(2)]
             check_decode(*c["out"], c["q"].cpu(), *flat, torch.arange(S).view(S, 1), torch.full((S,), i + 2), 0, 0)
     assert fa.fa_check_device_error() == 0
+
+
+def test_cache_of_more_than_2_to_the_32_elements(fa):
+    """Pages whose offsets pass 32 bits: appended to, read, forked, moved.  (Nothing else of the pool is touched.)"""
+    P, Hkv, page, d, S, M = 270_000, 8, 16, 128, 3, 8
+    kp, vp = (torch.empty(1, P, Hkv, page, d, dtype=torch.bfloat16, device="cuda") for _ in range(2))
+    assert kp.numel() > 2**32
+    i32 = lambda x: torch.tensor(x, dtype=torch.int32, device="cuda")
+    refs = torch.ones(P, dtype=torch.int32, device="cuda")         # all in use but the last ones and one early page
+    refs[-9:] = 0
+    refs[2] = 0
+    lens, table = i32([0] * S), torch.full((S, M), -1, dtype=torch.int32, device="cuda")
+    assert fa.cache.cache_reserve(refs, table, lens, i32([40, 0, 0]), page).item() == 0
+    assert table[0, :3].tolist() == [2, P - 9, P - 8]
+    g = torch.Generator().manual_seed(3)
+    k, v, q = (torch.randn(*s, generator=g).to(torch.bfloat16) for s in ((40, Hkv, d), (40, Hkv, d), (S, 16, d)))
+    fa.cache.cache_append(k.cuda(), v.cuda(), kp[0], vp[0], table, lens, i32([0, 40, 40, 40]))
+    assert torch.equal(kp[0, P - 8, :, 7].cpu(), k[39])
+    assert fa.cache.cache_fork(kp, vp, refs, table, lens, i32([0]), i32([2])).item() == 0
+    assert table[2, :3].tolist() == [2, P - 9, P - 7]
+    refs[10:16] = 0                                                # compaction brings the high pages down
+    live = fa.cache.cache_compact(kp, vp, refs, table, lens).item()
+    assert live == P - 6 - 6 and table[:, :3].max().item() < live
+    flat = [x.transpose(0, 1)[None].expand(S, -1, -1, -1) for x in (k, v)]
+    o, lse = fa.cache.attention_decode(q.cuda(), kp[0], vp[0], table, lens)
+    check_decode(o, lse, q, *flat, torch.arange(S).view(S, 1), torch.tensor([40, 0, 40]), 0, 0)
+    assert fa.fa_check_device_error() == 0
