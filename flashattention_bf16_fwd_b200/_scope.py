@@ -8,6 +8,8 @@ from __future__ import annotations
 
 import torch
 
+_raw_stream = torch._C._cuda_getCurrentRawStream
+
 
 def call(fn, t, stream, *args):
     """fn(*args, stream) with t's device current and ``stream`` (a torch stream or
@@ -18,9 +20,9 @@ def call(fn, t, stream, *args):
         raise ValueError("tensors must live on a CUDA device (the library has no CPU path)")
     if stream is None:
         if at == torch.cuda.current_device():
-            return fn(*args, torch._C._cuda_getCurrentRawStream(at))
+            return fn(*args, _raw_stream(at))
         with torch.cuda.device(at):
-            return fn(*args, torch._C._cuda_getCurrentRawStream(at))
+            return fn(*args, _raw_stream(at))
     if not isinstance(stream, torch.cuda.Stream):
         stream = (torch.cuda.ExternalStream(int(stream), device=t.device) if int(stream)
                   else torch.cuda.default_stream(t.device))
@@ -50,6 +52,9 @@ def int32(name, t, *shape):
                      f"[{', '.join('*' if n is None else str(n) for n in shape)}], got {t.dtype} {tuple(have)}")
 
 
+INT_MAX = 2**31 - 1
+
+
 def count(n) -> int:
-    """n as a C int: more than an int holds is as much as the largest one."""
-    return max(-1, min(int(n), 2**31 - 1))
+    """n as a C int: more than an int holds is as much as the largest one, less than nothing is -1."""
+    return n if 0 <= n <= INT_MAX else INT_MAX if n > 0 else -1

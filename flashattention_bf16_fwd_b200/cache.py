@@ -28,6 +28,7 @@ import functools
 import torch
 
 from . import _scope
+from ._scope import count as _count
 from .fa import _check, _elem, lib
 
 __all__ = ["EXPORTED", "fa_decode_workspace_size", "fa_cache_workspace_size", "attention_decode", "cache_append",
@@ -112,13 +113,13 @@ def attention_decode(q, k_pages, v_pages, table, lens, window: int | None = None
             and (workspace is None or workspace.get_device() == at)):
         raise ValueError("tensors must share one device")
     return _scope.call(_decode, q, stream, q, k_pages, v_pages, table, lens, workspace,
-                       (S, H, Hkv, d, P, page, M, stride, _scope.count(window or 0), _scope.count(sinks),
+                       (S, H, Hkv, d, P, page, M, stride, _count(window or 0), _count(sinks),
                         d ** -0.5 if scale is None else scale, _elem(q)))
 
 
 def _decode(q, k_pages, v_pages, table, lens, workspace, sizes, stream):
     S, H, Hkv, d = sizes[:4]
-    o = q.new_empty((S, H, d))
+    o = torch.empty_like(q) if q.is_contiguous() else q.new_empty((S, H, d))
     lse = q.new_empty((S, H), dtype=torch.float32)
     if workspace is None:
         workspace = q.new_empty(fa_decode_workspace_size(S, H, Hkv, d), dtype=torch.uint8)
@@ -173,7 +174,7 @@ def cache_reserve(refs, table, lens, add, page: int, stream=None):
     P, S, M = _page_tables(refs, table, lens)
     _scope.int32("add", add, S)
     _scope.same_device(refs, add)
-    return _scope.call(_reserve, refs, stream, refs, table, lens, add, (S, P, page, M))
+    return _scope.call(_reserve, refs, stream, refs, table, lens, add, (S, P, _count(page), M))
 
 
 def _reserve(refs, table, lens, add, sizes, stream):
@@ -218,7 +219,7 @@ def cache_free(refs, table, lens, seqs, page: int, stream=None):
     _scope.int32("seqs", seqs, None)
     _scope.same_device(refs, seqs)
     status = _scope.call(lib.fa_cache_free, refs, stream, refs.data_ptr(), table.data_ptr(), lens.data_ptr(),
-                         seqs.data_ptr(), seqs.shape[0], S, P, page, M)
+                         seqs.data_ptr(), seqs.shape[0], S, P, _count(page), M)
     if status:
         _check("fa_cache_free", status)
 
