@@ -482,9 +482,10 @@ __global__ void __launch_bounds__(384, 1)
             // is, and (kParts) P_bar V of the first 96 keys starts while the softmax
             // still works on the last 32: N = 16384, window 4096: 948 us with
             // neither, 864 with both; handed over after 64 keys 880, after 32 895.
-            // (The next S tile's second half before P_bar V, over columns that
-            // P_bar leaves free, is 1106: an N = 64 MMA is hardly shorter than an
-            // N = 128 one.)
+            // (What gained nothing: the next S tile's second half before P_bar V,
+            // over columns that P_bar leaves free, 1106, for an N = 64 MMA is hardly
+            // shorter than an N = 128 one; an issuer per warpgroup as at d = 64, 1090;
+            // the next item's first S before this one's last P_bar V, 893.)
             auto issue_pv_part = [&](int t, uint32_t st, bool first, int part) {
               const uint64_t b = sdesc_add(dv0, st * 2 * L::kTileBytes);
 #pragma unroll
