@@ -531,40 +531,40 @@ __global__ void __launch_bounds__(384, 1)
             }
             kv_cnt += w.nmax;
             for (int t = 0; t < 2; ++t) ep_cnt[t] += (nt[t] > 0) ? 1 : 0;
-            continue;
-          }
-          for (int t = 0; t < 2; ++t)
-            if (nt[t] > 0) issue_s(t, kv_cnt % L::kStages);
-          if (w.nmax == 1) umma_commit_warp(q_empty);
-          for (int j = 0; ok && j < w.nmax; ++j) {
-            const uint32_t st = (kv_cnt + j) % L::kStages;
-            const uint32_t stn = (kv_cnt + j + 1) % L::kStages;
-            for (int t = 0; t < 2; ++t) {
-              if (j < nt[t]) {
-                if (!(ok = wait(&p_full[t], (it_cnt[t] + j) & 1))) break;
-                // the first P_bar V of an item overwrites O_t: the previous
-                // item's epilogue must have read it
-                if (j == 0 && !(ok = wait(&o_free[t], (ep_cnt[t] & 1) ^ 1))) break;
-                tc_fence_after();
-                issue_pv(t, st, j);
-              }
-              if (t == 0 && j + 1 < w.nmax) {
-                const uint32_t nxt = kv_cnt + j + 1;
-                if (!(ok = wait(&kv_full[stn], (nxt / L::kStages) & 1))) break;
-                tc_fence_after();
-                if (j + 1 < nt[0]) issue_s(0, stn);   // S_0 of tile j+1 overwrites P_bar_0 after P_bar V
-              }
-              if (t == 1) {
-                umma_commit_warp(&kv_empty[st]);
-                if (j + 1 < nt[1]) issue_s(1, stn);
-                if (j + 2 == w.nmax) umma_commit_warp(q_empty);   // the item's last S MMAs are issued
+          } else {
+            for (int t = 0; t < 2; ++t)
+              if (nt[t] > 0) issue_s(t, kv_cnt % L::kStages);
+            if (w.nmax == 1) umma_commit_warp(q_empty);
+            for (int j = 0; ok && j < w.nmax; ++j) {
+              const uint32_t st = (kv_cnt + j) % L::kStages;
+              const uint32_t stn = (kv_cnt + j + 1) % L::kStages;
+              for (int t = 0; t < 2; ++t) {
+                if (j < nt[t]) {
+                  if (!(ok = wait(&p_full[t], (it_cnt[t] + j) & 1))) break;
+                  // the first P_bar V of an item overwrites O_t: the previous
+                  // item's epilogue must have read it
+                  if (j == 0 && !(ok = wait(&o_free[t], (ep_cnt[t] & 1) ^ 1))) break;
+                  tc_fence_after();
+                  issue_pv(t, st, j);
+                }
+                if (t == 0 && j + 1 < w.nmax) {
+                  const uint32_t nxt = kv_cnt + j + 1;
+                  if (!(ok = wait(&kv_full[stn], (nxt / L::kStages) & 1))) break;
+                  tc_fence_after();
+                  if (j + 1 < nt[0]) issue_s(0, stn);   // S_0 of tile j+1 overwrites P_bar_0 after P_bar V
+                }
+                if (t == 1) {
+                  umma_commit_warp(&kv_empty[st]);
+                  if (j + 1 < nt[1]) issue_s(1, stn);
+                  if (j + 2 == w.nmax) umma_commit_warp(q_empty);   // the item's last S MMAs are issued
+                }
               }
             }
-          }
-          kv_cnt += w.nmax;
-          for (int t = 0; t < 2; ++t) {
-            it_cnt[t] += nt[t];
-            ep_cnt[t] += (nt[t] > 0) ? 1 : 0;
+            kv_cnt += w.nmax;
+            for (int t = 0; t < 2; ++t) {
+              it_cnt[t] += nt[t];
+              ep_cnt[t] += (nt[t] > 0) ? 1 : 0;
+            }
           }
         }
         // Every MMA must be finished before TMEM is released.

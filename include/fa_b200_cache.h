@@ -113,7 +113,8 @@ FA_API int fa_cache_reserve(int32_t* refs, int32_t* table, int32_t* lens, const 
  *       Every dst is an empty slot (lens 0), and appears once.
  *   missing out : as in fa_cache_reserve; -1 also for a src or dst out of
  *       range, a dst that is not empty or appears twice.
- * All lengths are read before any is changed.
+ * All lengths are read before any is changed.  A page number out of range in a
+ * source's row is copied as it is, no page counted or read for it, and reported.
  *   workspace : fa_cache_workspace_size(S, P) bytes, as in fa_decode.
  */
 FA_API size_t fa_cache_workspace_size(int S, int P);

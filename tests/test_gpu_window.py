@@ -234,3 +234,35 @@ def test_prefill_then_decoding_behind_the_same_window(fa):
         within(o[0], want[0, :, i], tol[0, :, i], i)
         within(lse[0], want_lse[0, :, i], tol_lse[0, :, i], i)
     assert fa.fa_check_device_error() == 0
+
+
+def test_two_streams_at_once(fa):
+    """Training steps and decoding on two streams at the same time, each with its own tensors: as one after the other."""
+    from flashattention_bf16_fwd_b200 import cache
+    jobs = []
+    for seed, (H, Hkv, N, d, dt, win) in enumerate([(8, 4, 1500, 64, "bf16", 200), (6, 2, 1300, 128, "fp16", 333)]):
+        x = [t.cuda() for t in draw(2, H, Hkv, N, d, dt, seed)]
+        S, page = 40, 16
+        kp, vp = (torch.randn(400, Hkv, page, d, device="cuda").to(DT[dt]) for _ in range(2))
+        table = torch.randint(0, 400, (S, 20), dtype=torch.int32, device="cuda")
+        lens = torch.randint(0, 320, (S,), dtype=torch.int32, device="cuda")
+        qd = torch.randn(S, H, d, device="cuda").to(DT[dt])
+
+        def job(x=x, win=win, qd=qd, kp=kp, vp=vp, table=table, lens=lens):
+            o, lse = fa.window.attention_window_fwd(*x[:3], win, 4)
+            grads = fa.window.attention_window_bwd(*x[:3], o, lse, x[3], win, 4)
+            return (o, lse, *grads[1:], *cache.attention_decode(qd, kp, vp, table, lens))
+        jobs.append(job)
+    want = [job() for job in jobs]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in jobs]
+    for _ in range(10):
+        got = []
+        for job, stream in zip(jobs, streams):
+            with torch.cuda.stream(stream):
+                got.append([job() for _ in range(3)])
+        torch.cuda.synchronize()
+        for g, w in zip(got, want):
+            for one in g:
+                assert all(torch.equal(a, b) for a, b in zip(one, w))
+    assert fa.fa_check_device_error() == 0
