@@ -1,12 +1,19 @@
 """Devices, streams and argument checks that the bindings of the window and cache calls share.
 
 A call of this library takes some microseconds on the GPU for a single short
-sequence, so the bindings test everything in one expression and go through the
-checks below one by one only to say what is wrong.
+sequence.  So the usual call (current stream, current device, no workspace given)
+goes through the compiled module _fast, which returns None for any other; those,
+and calls that are wrong, take the way through ctypes and the checks below.
 """
 from __future__ import annotations
 
 import torch
+
+try:
+    from . import _fast  # noqa: F401
+except ImportError as e:
+    raise ImportError("the module _fast is missing or does not fit this torch: build it with "
+                      "`python -m flashattention_bf16_fwd_b200.build --force`") from e
 
 _raw_stream = torch._C._cuda_getCurrentRawStream
 
@@ -57,4 +64,5 @@ INT_MAX = 2**31 - 1
 
 def count(n) -> int:
     """n as a C int: more than an int holds is as much as the largest one, less than nothing is -1."""
+    n = int(n)
     return n if 0 <= n <= INT_MAX else INT_MAX if n > 0 else -1

@@ -28,6 +28,7 @@ import functools
 import torch
 
 from . import _scope
+from ._scope import _fast
 from ._scope import count as _count
 from .fa import _check, _elem, lib
 
@@ -100,6 +101,10 @@ def attention_decode(q, k_pages, v_pages, table, lens, window: int | None = None
     a fused projection are taken as they are), over the cache; returns
     (o [S, H, d], lse [S, H]).  ``window`` None or 0 shows every key; otherwise
     the last ``window`` keys and the first ``sinks``."""
+    if stream is None and workspace is None:
+        done = _fast.decode(q, k_pages, v_pages, table, lens, window, sinks, scale)
+        if done is not None:
+            return done
     if q.dim() != 3:
         raise ValueError("q must be [S, H, d]")
     P, Hkv, page, d = _pages(k_pages, v_pages, False)
@@ -134,6 +139,8 @@ def cache_append(k, v, k_pages, v_pages, table, lens, cu=None, stream=None):
     """Write the newest tokens, k and v [T, Hkv, d], of each sequence into one
     layer's pages: tokens cu[s] .. cu[s+1]-1 are the last ones of sequence s
     (``cu`` None: one token per sequence).  ``lens`` counts them already."""
+    if stream is None and _fast.append(k, v, k_pages, v_pages, table, lens, cu):
+        return
     P, Hkv, page, d = _pages(k_pages, v_pages, False)
     dtype = k_pages.dtype
     _elem(k_pages)
@@ -171,6 +178,10 @@ def cache_reserve(refs, table, lens, add, page: int, stream=None):
     """lens += add, with pages for the new tokens.  Returns ``missing``, int32
     [1] on the device: 0 when done, the number of pages lacking (nothing is
     changed then), or -1 (a length or an entry of add is out of range)."""
+    if stream is None:
+        missing = _fast.reserve(refs, table, lens, add, page)
+        if missing is not None:
+            return missing
     P, S, M = _page_tables(refs, table, lens)
     _scope.int32("add", add, S)
     _scope.same_device(refs, add)
@@ -190,6 +201,10 @@ def cache_fork(k_pages, v_pages, refs, table, lens, src, dst, stream=None, works
     """Sequence dst[f] (an empty slot) becomes a copy of sequence src[f]: full
     pages are shared, a last page that is not full is copied.  Returns
     ``missing`` as in cache_reserve."""
+    if stream is None and workspace is None:
+        missing = _fast.fork(k_pages, v_pages, refs, table, lens, src, dst)
+        if missing is not None:
+            return missing
     L, P, Hkv, page, d = _pages(k_pages, v_pages, True)
     _elem(k_pages)
     _, S, M = _page_tables(refs, table, lens, P)
@@ -215,6 +230,8 @@ def _fork(k_pages, v_pages, refs, table, lens, src, dst, workspace, sizes, strea
 def cache_free(refs, table, lens, seqs, page: int, stream=None):
     """End the sequences ``seqs`` (int32 [F]): their pages' counts fall by 1,
     their table entries become -1 and their lengths 0."""
+    if stream is None and _fast.free(refs, table, lens, seqs, page):
+        return
     P, S, M = _page_tables(refs, table, lens)
     _scope.int32("seqs", seqs, None)
     _scope.same_device(refs, seqs)
@@ -227,6 +244,10 @@ def cache_free(refs, table, lens, seqs, page: int, stream=None):
 def cache_compact(k_pages, v_pages, refs, table, lens, stream=None, workspace=None):
     """Move the pages in use to the numbers 0 .. live-1 (in all layers, with
     tables and counts).  Returns ``live``, int32 [1] on the device."""
+    if stream is None and workspace is None:
+        live = _fast.compact(k_pages, v_pages, refs, table, lens)
+        if live is not None:
+            return live
     L, P, Hkv, page, d = _pages(k_pages, v_pages, True)
     _elem(k_pages)
     _, S, M = _page_tables(refs, table, lens, P)

@@ -13,6 +13,7 @@ import functools
 import torch
 
 from . import _scope
+from ._scope import _fast
 from ._scope import count as _count
 from .fa import _check, _elem, _validate, lib
 
@@ -47,6 +48,10 @@ def _valid(q, k, v) -> bool:
 def attention_window_fwd(q, k, v, window: int, sinks: int = 0, scale: float | None = None, fix_mode: int = 1,
                          stream=None):
     """Allocate O and LSE and run the forward; returns (o, lse)."""
+    if stream is None:
+        done = _fast.window_fwd(q, k, v, window, sinks, scale, fix_mode)
+        if done is not None:
+            return done
     if not _valid(q, k, v):
         _validate(q, k, v)
     return _scope.call(_fwd, q, stream, q, k, v, window, sinks, scale, fix_mode, _elem(q))
@@ -68,6 +73,10 @@ def attention_window_bwd(q, k, v, o, lse, do, window: int, sinks: int = 0, scale
                          workspace=None):
     """Allocate dQ, dK, dV (and the workspace unless given) and run the
     backward of attention_window_fwd with the same window and sinks."""
+    if stream is None and workspace is None:
+        done = _fast.window_bwd(q, k, v, o, lse, do, window, sinks, scale)
+        if done is not None:
+            return done
     shape, dtype, at = q.shape, q.dtype, q.get_device()
     if not (_valid(q, k, v) and o.shape == shape and do.shape == shape and o.dtype is dtype and do.dtype is dtype
             and o.get_device() == at and do.get_device() == at and o.is_contiguous() and do.is_contiguous()):

@@ -454,3 +454,62 @@ def test_cache_of_more_than_2_to_the_32_elements(fa):
     o, lse = fa.cache.attention_decode(q.cuda(), kp[0], vp[0], table, lens)
     check_decode(o, lse, q, *flat, torch.arange(S).view(S, 1), torch.tensor([40, 0, 40]), 0, 0)
     assert fa.fa_check_device_error() == 0
+
+
+def test_both_ways_through_the_binding(fa, monkeypatch):
+    """The compiled way and the ctypes one give the same results, and the same errors."""
+    from flashattention_bf16_fwd_b200 import window
+    from flashattention_bf16_fwd_b200.fa import FAError
+    g = torch.Generator(device="cuda").manual_seed(1)
+    rand = lambda *s: torch.randn(*s, generator=g, device="cuda").half()
+    i32 = lambda x: torch.tensor(x, dtype=torch.int32, device="cuda")
+    q, k, v, do = rand(2, 4, 300, 64), rand(2, 2, 300, 64), rand(2, 2, 300, 64), rand(2, 4, 300, 64)
+    new_k, new_v, new_q = rand(90, 6, 64)[:, 2:4], rand(90, 2, 64), rand(4, 4, 64)
+
+    def everything():
+        kp, vp = (torch.zeros(2, 40, 2, 16, 64, dtype=torch.float16, device="cuda") for _ in range(2))
+        refs, lens, table = i32([0] * 40), i32([0] * 4), torch.full((4, 9), -1, dtype=torch.int32, device="cuda")
+        out = list(window.attention_window_fwd(q, k, v, 50, 3))
+        out += window.attention_window_bwd(q, k, v, *out, do, 50, 3, 0.2)[1:]
+        out.append(fa.cache.cache_reserve(refs, table, lens, i32([40, 33, 17, 0]), 16))
+        fa.cache.cache_append(new_k, new_v, kp[0], vp[0], table, lens, i32([0, 40, 73, 90, 90]))
+        out.append(fa.cache.cache_fork(kp, vp, refs, table, lens, i32([1]), i32([3])))
+        fa.cache.cache_append(new_k[:4], new_v[:4], kp[1], vp[1], table, lens)
+        out += fa.cache.attention_decode(new_q, kp[0], vp[0], table, lens, scale=0.3)
+        out += fa.cache.attention_decode(new_q, kp[0], vp[0], table, lens, window=9, sinks=2)
+        fa.cache.cache_free(refs, table, lens, i32([0]), 16)
+        out.append(fa.cache.cache_compact(kp, vp, refs, table, lens))
+        return out + [kp, vp, refs, table, lens]
+
+    def errors():
+        kp = torch.zeros(9, 2, 16, 64, dtype=torch.float16, device="cuda")
+        lens, table = i32([1]), i32([[0]])
+        said = []
+        for call in (lambda: window.attention_window_fwd(q, k, v, 0), lambda: window.attention_window_fwd(q, k, v, 5, -1),
+                     lambda: window.attention_window_fwd(q, k, v, 5, fix_mode=6),
+                     lambda: window.attention_window_fwd(q, k, v, 5, scale=-1.0), lambda: window.attention_window_fwd(q, k[:1], v, 5),
+                     lambda: window.attention_window_fwd(q, k.float(), v.float(), 5), lambda: window.attention_window_fwd(q, k.cpu(), v, 5),
+                     lambda: window.attention_window_bwd(q, k, v, q, do[..., 0], do, 5),
+                     lambda: fa.cache.attention_decode(new_q[:1], kp, kp, table, lens, sinks=3),
+                     lambda: fa.cache.attention_decode(new_q[:1], kp, kp, table, lens, window=-2),
+                     lambda: fa.cache.attention_decode(new_q[:2], kp, kp, table, lens),
+                     lambda: fa.cache.cache_append(new_k, new_v, kp, kp, table, lens),
+                     lambda: fa.cache.cache_reserve(i32([0] * 9), table, lens, lens, 12),
+                     lambda: fa.cache.cache_reserve(i32([0] * 9), table, lens, lens, 2**32 + 16),
+                     lambda: fa.cache.cache_free(i32([0] * 9), table, lens, i32([0, 0]), 16),
+                     lambda: fa.cache.cache_fork(kp, kp, i32([0] * 8), table, lens, lens, lens)):
+            with pytest.raises((ValueError, FAError)) as e:
+                call()
+            said.append((type(e.value), str(e.value)))
+        return said
+
+    fast, fast_errors = everything(), errors()
+    class Never:
+        def __getattr__(self, name):
+            return lambda *a: None
+    monkeypatch.setattr(fa.cache, "_fast", Never())
+    monkeypatch.setattr(window, "_fast", Never())
+    for a, b in zip(fast, everything()):
+        assert torch.equal(a, b)
+    assert errors() == fast_errors
+    assert fa.fa_check_device_error() == 0
