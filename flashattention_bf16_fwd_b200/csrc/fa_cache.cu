@@ -95,7 +95,8 @@ int launch_decode(const void* k_pages, const void* v_pages, DecodeParams prm, in
   if (launch(fa_decode_kernel<D, NB, E>, dim3(prm.ctas), dim3(DecLayout<D, NB>::kThreads),
              DecLayout<D, NB>::bytes(prm.S), stream, mk, mv, prm) != cudaSuccess)
     return FA_ERR_LAUNCH;
-  if (launch(fa_decode_join_kernel<D, NB, E>, dim3(prm.S * prm.H), dim3(128), 0, stream, prm) != cudaSuccess)
+  if (!prm.whole &&
+      launch(fa_decode_join_kernel<D, NB, E>, dim3(prm.S * prm.H), dim3(128), 0, stream, prm) != cudaSuccess)
     return FA_ERR_LAUNCH;
   return FA_OK;
 }
@@ -166,6 +167,11 @@ int fa_decode(const void* q, const void* k_pages, const void* v_pages, const int
   const long long most = (long long)S * prm.units * places;
   const int two = 2 * num_sms < kDecMaxCtas ? 2 * num_sms : kDecMaxCtas;
   prm.ctas = int(most < two ? most : two);
+  // The second launch costs 2 to 3 us, a tile more on a CTA's way 0.7 us: units are
+  // left whole where a table has room for up to 2 tiles (16 sequences of 2, H = 32
+  // over Hkv = 8, d = 128: 8.3 us, cut 10.5), or 4 where there are as many units as
+  // SMs (64 sequences: 16.8 us, cut 20.0; but 1 sequence of 4: 8.1, cut 7.6).
+  prm.whole = places - 1 <= 2 || (places - 1 <= 4 && (long long)S * prm.units >= num_sms);
   prm.scale_log2 = float(double(scale) * 1.4426950408889634);
   const cudaStream_t s = static_cast<cudaStream_t>(stream);
 #define FA_DECODE(D, NB) \

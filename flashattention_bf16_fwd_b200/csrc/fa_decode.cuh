@@ -17,7 +17,8 @@
 // unit that lies in one stretch is finished there; one that is cut leaves
 // unnormalised partial results (O, m, l), at most two per CTA, which
 // fa_decode_join_kernel puts together.  The cut depends on lens alone, so that
-// sums always run in the same order.
+// sums always run in the same order.  Where the table has room for few tiles per
+// sequence, units are left whole and the second launch is not made.
 //
 // A CTA: warp 4 fetches tiles with TMA into a ring, one box per page (or piece of
 // one) and 64 elements of d, with the queries in front of a unit's first tile;
@@ -50,7 +51,8 @@ struct DecodeParams {
   int P, page, M, box;      // box: keys per TMA box (a divisor of the tile and of the page)
   int z_none;               // a third TMA coordinate past the cache: the box reads as zeros
   int window, sinks;
-  int ctas;                 // CTAs that the tiles are divided among
+  int ctas;                 // CTAs that the places are divided among
+  int whole;                // no unit is cut: a stretch begins and ends with one
   float scale_log2;
 };
 
@@ -253,11 +255,20 @@ __global__ void __launch_bounds__(160, 2)
   }
 
   const long long total = (long long)cum[p.S] * p.units;
-  const long long x0 = dec_cut(total, p.ctas, blockIdx.x), x1 = dec_cut(total, p.ctas, blockIdx.x + 1);
-  const int n = int(x1 - x0);
-  if (n == 0) return;
-  const Watchdog wd{abort_flag, p.dev_error};
+  long long x0 = dec_cut(total, p.ctas, blockIdx.x), x1 = dec_cut(total, p.ctas, blockIdx.x + 1);
+  if (x0 == x1) return;
   DecWalk w;
+  if (p.whole) {                      // both on to the next unit's first place
+    w.start(cum, p.S, p.units, x0);
+    if (w.t) x0 += w.nt + 1 - w.t;
+    if (x1 < total) {
+      w.start(cum, p.S, p.units, x1);
+      if (w.t) x1 += w.nt + 1 - w.t;
+    }
+  }
+  const int n = int(x1 - x0);
+  if (n <= 0) return;
+  const Watchdog wd{abort_flag, p.dev_error};
   w.start(cum, p.S, p.units, x0);
   // the query heads of a unit: the first one, and how many
   auto heads = [&](const DecWalk& u, int& h0, int& nh) {
