@@ -107,92 +107,89 @@ __global__ void __launch_bounds__(256) fa_cache_append_kernel(const AppendParams
 // planning, one CTA of kPlanThreads
 // ---------------------------------------------------------------------------
 // The sum of x over the CTA's threads before this one; `total` gets the sum of
-// all.  `sums`: 33 ints of shared memory.
-__device__ __forceinline__ int cta_scan(int x, int* sums, int& total) {
+// all.  `sums`: 32 values of shared memory.
+template <typename T>
+__device__ __forceinline__ T cta_scan(T x, T* sums, T& total) {
   const int lane = int(lane_id()), warp = int(warp_id());
-  int inc = x;
+  T inc = x;
 #pragma unroll
   for (int d = 1; d < 32; d <<= 1) {
-    const int up = __shfl_up_sync(0xffffffffu, inc, d);
+    const T up = __shfl_up_sync(0xffffffffu, inc, d);
     if (lane >= d) inc += up;
   }
   __syncthreads();                                 // the previous scan's sums have been read
   if (lane == 31) sums[warp] = inc;
   __syncthreads();
   if (warp == 0) {
-    int y = sums[lane];
+    T y = sums[lane];
 #pragma unroll
     for (int d = 1; d < 32; d <<= 1) {
-      const int up = __shfl_up_sync(0xffffffffu, y, d);
+      const T up = __shfl_up_sync(0xffffffffu, y, d);
       if (lane >= d) y += up;
     }
     sums[lane] = y;
   }
   __syncthreads();
   total = sums[31];
-  return (warp ? sums[warp - 1] : 0) + inc - x;
+  return (warp ? sums[warp - 1] : T(0)) + inc - x;
 }
 
-// Visits the pages [from, to) in ascending order, 4 per thread and round, and
-// calls take(rank, page) for those that are free (kFree) or in use (!kFree),
-// rank counting them from 0, until `most` have been found.  Returns how many
-// were found (at least `most` if there are so many).
-template <bool kFree, typename F>
-__device__ __forceinline__ int visit_pages(const int32_t* refs, int from, int to, int most, int* sums, F take) {
-  int found = 0;
-  for (int base = from & ~3; base < to && found < most; base += 4 * kPlanThreads) {
-    const int at = base + 4 * int(threadIdx.x);
-    int r[4] = {0, 0, 0, 0};
-    if (at >= from && at + 4 <= to) {
-      const int4 v = *reinterpret_cast<const int4*>(refs + at);
-      r[0] = v.x;
-      r[1] = v.y;
-      r[2] = v.z;
-      r[3] = v.w;
+// Two counts scanned at once, as the halves of a word.
+using Pair = unsigned long long;
+__device__ __forceinline__ Pair pair_of(int hi, int lo) { return Pair(unsigned(hi)) << 32 | unsigned(lo); }
+__device__ __forceinline__ int hi_of(Pair x) { return int(x >> 32); }
+__device__ __forceinline__ int lo_of(Pair x) { return int(unsigned(x)); }
+
+// The four pages of thread i in the round that begins at page `base`: which are
+// free (count 0, or below: a corrupt one) and which in use, as bits.  (16 pages a
+// thread make fewer rounds of a large pool, but a thread then hands out up to 16
+// pages one after the other: a fork among 1300 pages 9.5 us instead of 7.1.)
+constexpr int kPer = 4;
+constexpr int kRound = kPer * kPlanThreads;
+struct Pages {
+  int first;
+  unsigned free_bits, used_bits;
+  __device__ __forceinline__ Pages(const int32_t* refs, int P, int base)
+      : first(base + kPer * int(threadIdx.x)), free_bits(0), used_bits(0) {
+    if (first + kPer <= P) {
+      const int4 v = *reinterpret_cast<const int4*>(refs + first);
+      used_bits = (v.x > 0 ? 1u : 0u) | (v.y > 0 ? 2u : 0u) | (v.z > 0 ? 4u : 0u) | (v.w > 0 ? 8u : 0u);
+      free_bits = ~used_bits & 15u;
     } else {
-#pragma unroll
-      for (int i = 0; i < 4; ++i)
-        if (at + i >= from && at + i < to) r[i] = refs[at + i];
+      for (int i = 0; first + i < P; ++i) (refs[first + i] > 0 ? used_bits : free_bits) |= 1u << i;
     }
-    bool hit[4];
-    int n = 0;
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      hit[i] = at + i >= from && at + i < to && (kFree ? r[i] <= 0 : r[i] > 0);
-      n += hit[i];
-    }
-    int total;
-    int rank = found + cta_scan(n, sums, total);
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-      if (hit[i] && rank < most) {
-        take(rank, at + i);
-        ++rank;
-      }
+  }
+};
+
+// Calls take(rank, page) for the free pages in ascending order, rank counting
+// them from 0, until `most` have been taken.
+template <typename F>
+__device__ __forceinline__ void take_free(const CacheParams& p, int most, int* sums, F take) {
+  int found = 0;
+  for (int base = 0; base < p.P && found < most; base += kRound) {
+    const Pages q(p.refs, p.P, base);
+    int total, rank = found + cta_scan(__popc(q.free_bits), sums, total);
+    for (unsigned left = q.free_bits; left && rank < most; left &= left - 1, ++rank) take(rank, q.first + __ffs(left) - 1);
     found += total;
   }
-  return found;
+}
+
+__device__ __forceinline__ int count_pages(const CacheParams& p, bool used, int* sums) {
+  int n = 0, total;
+#pragma unroll 4
+  for (int base = 0; base < p.P; base += kRound) {
+    const Pages q(p.refs, p.P, base);
+    n += __popc(used ? q.used_bits : q.free_bits);
+  }
+  cta_scan(n, sums, total);
+  return total;
 }
 
 __device__ __forceinline__ int pages_of(const CacheParams& p, int len) { return (len + p.page - 1) / p.page; }
 
-// need[i] = pages wanted by request i, i < n (in shared memory) -> need[i] =
-// pages wanted before request i; returns the total.
-__device__ __forceinline__ int scan_needs(int* need, int n, int* sums) {
-  int before = 0;
-  for (int base = 0; base < n; base += kPlanThreads) {
-    const int i = base + int(threadIdx.x);
-    const int x = i < n ? need[i] : 0;
-    int total;
-    const int at = cta_scan(x, sums, total);
-    if (i < n) need[i] = before + at;
-    before += total;
-  }
-  __syncthreads();
-  return before;
-}
-
-// The request that page `rank` belongs to: the last i with need[i] <= rank.
+// The request that page `rank` belongs to, where need[i] pages are wanted before
+// request i: the last i with need[i] <= rank (several may begin at one rank; the
+// last of them wants it).
 __device__ __forceinline__ int request_of(const int* need, int n, int rank) {
   int a = 0, b = n;
   while (b - a > 1) {
@@ -202,11 +199,47 @@ __device__ __forceinline__ int request_of(const int* need, int n, int rank) {
   return a;
 }
 
+// need[i] = pages wanted by request i (in shared memory, i < n) -> pages wanted
+// before it, and the free pages handed out by take(rank, page) if there are
+// enough.  Returns how many are missing.  One scan over both counts where one
+// round covers the requests and its pages are enough: a step of a serving loop
+// waits for this CTA, and a scan's barriers and a load of the counts are each
+// about a tenth of its time.
+template <typename F>
+__device__ __forceinline__ int hand_out(const CacheParams& p, int* need, int n, F take) {
+  __shared__ Pair pair_sums[32];
+  __shared__ int sums[32];
+  const Pages q(p.refs, p.P, 0);
+  const int i = int(threadIdx.x);
+  Pair total;
+  const Pair before = cta_scan(pair_of(i < n ? need[i] : 0, __popc(q.free_bits)), pair_sums, total);
+  if (n <= kPlanThreads && hi_of(total) <= lo_of(total)) {
+    if (i < n) need[i] = hi_of(before);
+    __syncthreads();
+    int rank = lo_of(before);
+    for (unsigned left = q.free_bits; left && rank < hi_of(total); left &= left - 1, ++rank)
+      take(rank, q.first + __ffs(left) - 1);
+    return 0;
+  }
+  int wanted = 0;
+  for (int base = 0; base < n; base += kPlanThreads) {
+    const int x = base + i < n ? need[base + i] : 0;
+    int round;
+    const int at = cta_scan(x, sums, round);
+    if (base + i < n) need[base + i] = wanted + at;
+    wanted += round;
+  }
+  const int have = count_pages(p, false, sums);
+  if (have < wanted) return wanted - have;
+  __syncthreads();                                 // every count and need has been read and written
+  take_free(p, wanted, sums, take);
+  return 0;
+}
+
 // reserve: one CTA.  Dynamic shared memory: S ints.
 __global__ void __launch_bounds__(kPlanThreads) fa_cache_reserve_kernel(const CacheParams p, const int32_t* add,
                                                                         int32_t* missing) {
   extern __shared__ int need[];
-  __shared__ int sums[33];
   grid_dep_wait();
   grid_dep_launch();
   bool bad = false;
@@ -223,21 +256,15 @@ __global__ void __launch_bounds__(kPlanThreads) fa_cache_reserve_kernel(const Ca
     }
     return;
   }
-  const int total = scan_needs(need, p.S, sums);
-  const int have = visit_pages<true>(p.refs, 0, p.P, total, sums, [](int, int) {});
-  if (have < total) {
-    if (threadIdx.x == 0) *missing = total - have;
-    return;
-  }
-  __syncthreads();                                 // every count has been read
-  visit_pages<true>(p.refs, 0, p.P, total, sums, [&](int rank, int page) {
+  const int lacking = hand_out(p, need, p.S, [&](int rank, int page) {
     const int s = request_of(need, p.S, rank);
     p.table[size_t(s) * p.M + pages_of(p, p.lens[s]) + rank - need[s]] = page;
     p.refs[page] = 1;
   });
   __syncthreads();                                 // the old lengths have been read
-  for (int s = threadIdx.x; s < p.S; s += kPlanThreads) p.lens[s] += add[s];
-  if (threadIdx.x == 0) *missing = 0;
+  if (lacking == 0)
+    for (int s = threadIdx.x; s < p.S; s += kPlanThreads) p.lens[s] += add[s];
+  if (threadIdx.x == 0) *missing = lacking;
 }
 
 // One fork: dst takes `whole` shared pages of src and, if rest > 0, page `to`
@@ -254,7 +281,6 @@ __global__ void __launch_bounds__(kPlanThreads) fa_cache_fork_plan_kernel(const 
   extern __shared__ int need[];
   int* len = need + F;
   unsigned* taken = reinterpret_cast<unsigned*>(len + F);
-  __shared__ int sums[33];
   grid_dep_wait();
   grid_dep_launch();
   for (int i = threadIdx.x; i < (p.S + 31) / 32; i += kPlanThreads) taken[i] = 0;
@@ -280,34 +306,24 @@ __global__ void __launch_bounds__(kPlanThreads) fa_cache_fork_plan_kernel(const 
     }
     return;
   }
-  const int total = scan_needs(need, F, sums);
-  const int have = visit_pages<true>(p.refs, 0, p.P, total, sums, [](int, int) {});
-  if (have < total) {
-    if (threadIdx.x == 0) *missing = total - have;
-    return;
-  }
-  for (int f = threadIdx.x; f < F; f += kPlanThreads) {
-    ForkPlan e;
-    e.src = src[f];
-    e.dst = dst[f];
-    e.whole = len[f] / p.page;
-    e.rest = len[f] % p.page;
-    e.from = e.rest ? p.table[size_t(e.src) * p.M + e.whole] : -1;
-    e.to = -1;
-    plan[f] = e;
-    p.lens[e.dst] = len[f];
-  }
-  __syncthreads();
-  visit_pages<true>(p.refs, 0, p.P, total, sums, [&](int rank, int page) {
-    const int f = request_of(need, F, rank);       // several requests may start at one rank: the last of them needs it
+  const int lacking = hand_out(p, need, F, [&](int rank, int page) {
+    const int f = request_of(need, F, rank);
     plan[f].to = page;
-    p.table[size_t(plan[f].dst) * p.M + plan[f].whole] = page;
+    p.table[size_t(dst[f]) * p.M + len[f] / p.page] = page;
     p.refs[page] = 1;
   });
-  if (threadIdx.x == 0) {
-    *plan_n = F;
-    *missing = 0;
+  if (threadIdx.x == 0) *missing = lacking;
+  if (lacking) return;
+  for (int f = threadIdx.x; f < F; f += kPlanThreads) {
+    ForkPlan* e = plan + f;                        // `to` is written above
+    e->src = src[f];
+    e->dst = dst[f];
+    e->whole = len[f] / p.page;
+    e->rest = len[f] % p.page;
+    e->from = e->rest ? p.table[size_t(e->src) * p.M + e->whole] : -1;
+    p.lens[e->dst] = len[f];
   }
+  if (threadIdx.x == 0) *plan_n = F;
 }
 
 // fork, second kernel: CTA (f, y) copies the used tokens of fork f's last page
@@ -378,20 +394,43 @@ __global__ void __launch_bounds__(256) fa_cache_free_kernel(const CacheParams p,
 
 // compact, first kernel: one CTA.  Writes the moves (source pages, and their
 // destinations) and which move each source page is; counts move with the pages.
+// With u(x) pages in use before page x, a free page x < live is the destination
+// number x - u(x), and a used page x >= live the source number u(x) - u(live).
 __global__ void __launch_bounds__(kPlanThreads) fa_cache_compact_plan_kernel(const CacheParams p, int32_t* live_out,
                                                                              int32_t* moves, int32_t* from,
                                                                              int32_t* to, int32_t* went) {
-  __shared__ int sums[33];
+  __shared__ int sums[32];
+  __shared__ int u_live;
   grid_dep_wait();
   grid_dep_launch();
-  const int live = visit_pages<false>(p.refs, 0, p.P, p.P, sums, [](int, int) {});
-  const int n = visit_pages<false>(p.refs, live, p.P, p.P, sums, [&](int rank, int page) { from[rank] = page; });
+  const int live = count_pages(p, true, sums);
+  if (threadIdx.x == 0) u_live = live;             // where all pages are in use, and none moves
+  int used = 0;
+  Pages next(p.refs, p.P, 0);
+  for (int base = 0; base < p.P; base += kRound) {
+    const Pages q = next;
+    next = Pages(p.refs, p.P, base + kRound);      // on its way during this round's scan
+    int total;
+    int u = used + cta_scan(__popc(q.used_bits), sums, total);
+    if (live >= q.first && live < q.first + kPer) u_live = u + __popc(q.used_bits & ((1u << (live - q.first)) - 1u));
+    __syncthreads();                               // u(live) is known from its round on
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) {
+      const int x = q.first + i;
+      const bool in_use = q.used_bits >> i & 1u;
+      if (x < live && !in_use) to[x - u] = x;      // (live <= P)
+      if (x >= live && in_use) {
+        from[u - u_live] = x;
+        went[x] = u - u_live;
+      }
+      u += in_use;
+    }
+    used += total;
+  }
   __syncthreads();
-  visit_pages<true>(p.refs, 0, live, n, sums, [&](int rank, int page) { to[rank] = page; });
-  __syncthreads();
+  const int n = live - u_live;                     // as many pages in use past live as free ones before it
   for (int i = threadIdx.x; i < n; i += kPlanThreads) {
     const int a = from[i], b = to[i];
-    went[a] = i;
     p.refs[b] = p.refs[a];
     p.refs[a] = 0;
   }
@@ -401,8 +440,7 @@ __global__ void __launch_bounds__(kPlanThreads) fa_cache_compact_plan_kernel(con
   }
 }
 
-// compact, second kernel: the moves in all layers, K and V, one piece of a page
-// per CTA and round, and the tables.
+// compact, second kernel: the moves in all layers, K and V, and the tables.
 __global__ void __launch_bounds__(256) fa_cache_compact_copy_kernel(const CacheParams p, const int32_t* live,
                                                                     const int32_t* moves, const int32_t* from,
                                                                     const int32_t* to, const int32_t* went) {
@@ -422,26 +460,28 @@ __global__ void __launch_bounds__(256) fa_cache_compact_copy_kernel(const CacheP
     else
       cache_error(p);
   }
+  // A group of threads has four words each under way: the CTA where a page is 16 KB
+  // or more (8 layers of 32 KB pages: 158 us, warp by warp 161), a warp where it is
+  // less, so that as many pages are (4160 moves of 2 KB pages: 33 us, by CTAs 39).
+  // All pieces of a pool that fits a GPU are below 2^32.
   const long long page = (long long)p.hkv * p.page << p.row_log2;   // words of a page in one layer
-  constexpr int kPiece = 256 * 4;                                   // words that a CTA has in flight
-  const long long pieces = (page + kPiece - 1) / kPiece;
-  const long long items = 2ll * p.L * n * pieces;
-  for (long long it = blockIdx.x; it < items; it += gridDim.x) {
-    const long long piece = it % pieces;
-    const int m = int(it / pieces % n);
-    const int lv = int(it / pieces / n);                            // layer, K or V
-    uint4* pool = (lv & 1) ? p.v_pages : p.k_pages;
+  const int width = page >= 1024 ? 256 : 32, lane = int(threadIdx.x) % width;
+  const unsigned pieces = unsigned((page + 4 * width - 1) / (4 * width));
+  const unsigned items = 2u * unsigned(p.L) * unsigned(n) * pieces, groups = unsigned(256 / width);
+  for (unsigned it = blockIdx.x * groups + threadIdx.x / width; it < items; it += gridDim.x * groups) {
+    const unsigned piece = it % pieces, mv = it / pieces, m = mv % unsigned(n), lv = mv / unsigned(n);
+    uint4* pool = (lv & 1) ? p.v_pages : p.k_pages;                 // lv: layer, K or V
     const uint4* a = pool + ((long long)(lv >> 1) * p.P + from[m]) * page;
     uint4* b = pool + ((long long)(lv >> 1) * p.P + to[m]) * page;
     uint4 x[4];
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      const long long w = piece * kPiece + i * 256 + threadIdx.x;
+      const long long w = ((long long)piece * 4 + i) * width + lane;
       if (w < page) x[i] = a[w];
     }
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      const long long w = piece * kPiece + i * 256 + threadIdx.x;
+      const long long w = ((long long)piece * 4 + i) * width + lane;
       if (w < page) b[w] = x[i];
     }
   }

@@ -321,6 +321,21 @@ def test_large_pool_scan(fa):
     b.check()
 
 
+def test_more_sequences_than_planning_threads(fa):
+    """Requests beyond one round of the planning kernel, with and without enough pages."""
+    P, S, M, page = 5000, 2500, 4, 8
+    b = Both(fa, 1, P, 1, page, 64, S, M, 4)
+    assert b.reserve([(5 * s) % 24 if s < 1250 else 0 for s in range(S)]) == 0
+    assert b.fork([(3 * f) % 1250 for f in range(1150)], list(range(1300, 2450))) == 0
+    b.check()
+    assert b.reserve([8 if n <= 24 else 0 for n in b.n]) > 0          # too many
+    b.check()
+    b.free(list(range(0, 1250, 2)))
+    assert b.reserve([s % 2 for s in range(S)]) == 0
+    b.compact()
+    b.check()
+
+
 def test_serving_run(fa):
     """Prompts, decoding, branches, ended sequences and compaction, as a server does them: every step's
     attention equals the plain one over each sequence's own tokens."""
