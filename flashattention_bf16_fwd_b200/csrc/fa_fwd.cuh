@@ -165,11 +165,12 @@ __device__ __forceinline__ constexpr float rounds_to_one() {
 // (near ties) and with the debug records (tie record, P_bar == 1 count, O
 // before rounding); the other instantiation, used for fix_mode 0-3 without
 // records, leaves all of it out.
-// kWin: the windowed kernel, in which each query sees the keys of its window and
-// the sinks: the same pipeline over a shorter list of key tiles.  Without
-// kVariants it is fix_mode 1's, with a softmax of its own; the other fix_modes
-// take the kVariants instantiation, whose softmax is the one below.
-template <int D, bool kVariants, typename E = ElemBF16, bool kWin = false>
+// kWin: the windowed kernel (1, 2), in which each query sees the keys of its
+// window and the sinks: the same pipeline over a shorter list of key tiles.
+// 2 is fix_mode 1's, whose shift stays above the maximum; 1 shifts by the exact
+// maximum, without kVariants for fix_mode 0, which needs to know nothing else of
+// the row, with it for 2 to 5.  Each has a softmax of its own.
+template <int D, bool kVariants, typename E = ElemBF16, int kWin = 0>
 __global__ void __launch_bounds__(384, 1)
     fa_fwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
                   const __grid_constant__ CUtensorMap tm_v, const __grid_constant__ CUtensorMap tm_o,
@@ -195,7 +196,7 @@ __global__ void __launch_bounds__(384, 1)
   // kv_empty are K's), so that K of the next key tile is there while P_bar V of
   // this one is waited for; and P_bar is handed over in two parts
   constexpr bool kSplitKV = kWin && !L::kSepP;
-  constexpr bool kParts = kSplitKV && !kVariants;
+  constexpr bool kParts = kSplitKV && kWin == 2;
   uint64_t* v_full = mma_done + 2;                  // [kStages]
   uint64_t* v_empty = v_full + (kSplitKV ? L::kStages : 0);
   uint64_t* p_most = v_empty + (kSplitKV ? L::kStages : 0);   // [2] the first 96 keys of P_bar are written
@@ -630,7 +631,17 @@ __global__ void __launch_bounds__(384, 1)
         for (int i = 0; i < 128; ++i) s[i] = __uint_as_float(r[i >> 5][i & 31]);
 
         const int key0 = (kWin ? fwd_key_tile(w, j + (skip >= 0 && j >= skip ? 1 : 0)) : j) * 128;
-        if constexpr (kWin && !kVariants) {
+        // windowed kernel: does some row of the warp not see every key of the tile?
+        [[maybe_unused]] const int row0 = row - lane;
+        [[maybe_unused]] bool edge_tile = false;
+        if constexpr (kWin)
+          edge_tile = key0 + 127 > min(row0, p.N - 1) || (key0 + 127 >= p.sinks && key0 < row0 + 32 - p.window);
+        // the 32 keys of piece c of the tile that the row sees, as bits
+        [[maybe_unused]] auto seen_bits = [&](int c) {
+          const int first = key0 + 32 * c;
+          return low_bits(limit + 1 - first) & (~low_bits(row - p.window + 1 - first) | low_bits(p.sinks - first));
+        };
+        if constexpr (kWin == 2) {
           // fix_mode 1 with a shift that stays above the running maximum.  The
           // shift is set to the maximum + delta + kHeadroom and left there until
           // the maximum + delta passes it, so that every exponential is below 1
@@ -658,8 +669,7 @@ __global__ void __launch_bounds__(384, 1)
             for (int c = 0; c < 4; ++c) {
               mx[2 * c] = mx[2 * c + 1] = kNegInf;
               if constexpr (kEdge) {
-                const int hi = limit - key0, lo = row - p.window + 1 - key0, sk = p.sinks - key0;
-                const uint32_t see = low_bits(hi + 1 - 32 * c) & (~low_bits(lo - 32 * c) | low_bits(sk - 32 * c));
+                const uint32_t see = seen_bits(c);
                 any[c] = __any_sync(0xffffffffu, see != 0u);
                 if (any[c] && __any_sync(0xffffffffu, see != 0xffffffffu)) {
 #pragma unroll
@@ -739,8 +749,7 @@ __global__ void __launch_bounds__(384, 1)
             l = l * alpha + (ea + eb);
             return true;
           };
-          const int row0 = row - lane;                 // the warp's first row
-          if (key0 + 127 > min(row0, p.N - 1) || (key0 + 127 >= p.sinks && key0 < row0 + 32 - p.window))
+          if (edge_tile)
             ok = tile(std::true_type{});
           else
             ok = tile(std::false_type{});
@@ -750,17 +759,20 @@ __global__ void __launch_bounds__(384, 1)
           mbar_arrive(&p_full[t]);
           continue;
         }
-        const bool masked = key0 + 127 > limit;
-        if (masked) {
-#pragma unroll
-          for (int i = 0; i < 128; ++i) s[i] = (key0 + i > limit) ? kNegInf : s[i];
-        }
         if constexpr (kWin) {
-          // keys before the window that are no sinks: numbers a .. b - 1 of the tile
-          const int a = max(0, p.sinks - key0), b = row - p.window + 1 - key0;
-          if (a < b && a < 128) {
+          if (edge_tile) {
 #pragma unroll
-            for (int i = 0; i < 128; ++i) s[i] = (i >= a && i < b) ? kNegInf : s[i];
+            for (int c = 0; c < 4; ++c) {
+              const uint32_t see = seen_bits(c);
+#pragma unroll
+              for (int i = 0; i < 32; ++i) s[32 * c + i] = (see >> i & 1u) ? s[32 * c + i] : kNegInf;
+            }
+          }
+        } else {
+          const bool masked = key0 + 127 > limit;
+          if (masked) {
+#pragma unroll
+            for (int i = 0; i < 128; ++i) s[i] = (key0 + i > limit) ? kNegInf : s[i];
           }
         }
         // tile maximum: eight 16-wide 3-input max chains, then a short tree
@@ -775,6 +787,130 @@ __global__ void __launch_bounds__(384, 1)
         const float mt = fmax3(fmax3(mx[0], mx[1], mx[2]), fmax3(mx[3], mx[4], mx[5]), fmaxf(mx[6], mx[7]));
         const float m_new = fmaxf(m, mt);
         const float ms_new = (m_new == kNegInf) ? 0.f : m_new * sl2;
+        if constexpr (kWin == 1) {
+          // The softmax below, bit for bit, with what it finds out about the row's
+          // largest entries found first, so that a quarter of the tile is packed
+          // and stored as soon as its exponentials are there, and a quarter of O_t
+          // rescaled behind it (prefill of 16384 tokens, 32 heads of 128, window
+          // 4096: fix_mode 0 1708 -> 1032 us, 2 1774 -> 1266, 5 2038 -> 1291).
+          bool raise = false, raise_early = false;
+          [[maybe_unused]] int c_new = 0, cn_new = 0;
+          [[maybe_unused]] float s2_new = kNegInf;
+          if constexpr (kVariants) {
+            if (p.fix) {
+              // The second largest entry, which is the largest again where that is
+              // repeated.  As an 8 x 16 grid the two largest lie in different rows
+              // or in different columns, so that it is the second largest of the
+              // rows' or of the columns' maxima.
+              float hi = mx[0], s2t = kNegInf;
+#pragma unroll
+              for (int g = 1; g < 8; ++g) {
+                s2t = fmaxf(s2t, fminf(hi, mx[g]));
+                hi = fmaxf(hi, mx[g]);
+              }
+              hi = kNegInf;
+#pragma unroll
+              for (int g = 0; g < 16; ++g) {
+                const float x = fmax3(fmax3(s[g], s[16 + g], s[32 + g]), fmax3(s[48 + g], s[64 + g], s[80 + g]),
+                                      fmaxf(s[96 + g], s[112 + g]));
+                s2t = fmaxf(s2t, fminf(hi, x));
+                hi = fmaxf(hi, x);
+              }
+              if (p.near) {
+                s2_new = (m > mt) ? fmaxf(s2, mt) : ((mt > m) ? fmaxf(m, s2t) : mt);
+                cn_new = (s2_new != kNegInf && ex2(fmaf(s2_new, sl2, -ms_new)) >= rounds_to_one<E>()) ? 2 : 0;
+              } else if (m_new != kNegInf) {
+                c_new = (m == m_new ? cnt : 0) + (mt == m_new ? (s2t == mt ? 2 : 1) : 0);
+              }
+              raise = (p.near ? cn_new : c_new) >= 2;
+              raise_early = m == m_new && (p.near ? cnt_near : cnt) >= 2;
+            }
+          }
+          const float msh = raise_early ? ms_new + p.delta_log2 : ms_new;
+          // a row raised in this tile is packed scaled by 2^-delta
+          const float pf = (raise && !raise_early) ? kFixFactor : 1.f;
+          // nothing seen so far: ms is no shift, and O and l are 0
+          float alpha = (m == kNegInf) ? 0.f : ex2(ms - ms_new);
+          if (kVariants && raise != raised) alpha = raise ? alpha * kFixFactor : alpha / kFixFactor;
+          // P_bar V of the tile before must be finished: it read the P_bar buffer
+          // and O_t must hold its result before O_t is rescaled
+          if (j > 0) {
+            ok = __all_sync(0xffffffffu, mbar_wait(&o_done[t], (it_cnt + j - 1) & 1, wd));
+            if (!ok) break;
+            tc_fence_after();
+          }
+          const bool rescale = j > 0 && __any_sync(0xffffffffu, alpha != 1.f);
+          const uint64_t sl2_2 = f2_pack(sl2, sl2), nmsh_2 = f2_pack(-msh, -msh), a2 = f2_pack(alpha, alpha);
+          [[maybe_unused]] const uint64_t pf2 = f2_pack(pf, pf);
+          uint64_t sum2[4] = {0, 0, 0, 0};
+          [[maybe_unused]] float rs_bar = 0.f;
+          uint32_t o[D / 4];
+          auto load_o = [&](int c) {
+            if constexpr (D == 128)
+              tmem_ld32(t_o + c * 32, o);
+            else
+              tmem_ld16(t_o + c * 16, o);
+          };
+          auto store_o = [&](int c) {
+            tmem_ld_wait(o);
+#pragma unroll
+            for (int i = 0; i < D / 8; ++i) {
+              float y0, y1;
+              f2_unpack(f2_mul(f2_pack(__uint_as_float(o[2 * i]), __uint_as_float(o[2 * i + 1])), a2), y0, y1);
+              o[2 * i] = __float_as_uint(y0);
+              o[2 * i + 1] = __float_as_uint(y1);
+            }
+            if constexpr (D == 128)
+              tmem_st32(t_o + c * 32, o);
+            else
+              tmem_st16(t_o + c * 16, o);
+          };
+#pragma unroll
+          for (int c = 0; c < 4; ++c) {
+            uint32_t pk[16];
+#pragma unroll
+            for (int i = 0; i < 16; ++i) {
+              float x0, x1;
+              f2_unpack(f2_fma(f2_pack(s[32 * c + 2 * i], s[32 * c + 2 * i + 1]), sl2_2, nmsh_2), x0, x1);
+              x0 = ex2(x0);
+              x1 = ex2(x1);
+              sum2[i & 3] = f2_add(sum2[i & 3], f2_pack(x0, x1));
+              if constexpr (kVariants) f2_unpack(f2_mul(f2_pack(x0, x1), pf2), x0, x1);
+              pk[i] = E::pack(x0, x1);
+            }
+            if (kVariants && p.self_norm) {
+#pragma unroll
+              for (int i = 0; i < 16; ++i) {
+                const float2 pp = E::unpack(pk[i]);
+                rs_bar += pp.x + pp.y;
+              }
+            }
+            tmem_st16(t_p + c * 16, pk);
+            if (rescale) {
+              if (c > 0) store_o(c - 1);
+              load_o(c);
+            }
+          }
+          if (rescale) store_o(3);
+          float ea, eb;
+          f2_unpack(f2_add(f2_add(sum2[0], sum2[1]), f2_add(sum2[2], sum2[3])), ea, eb);
+          float rs = ea + eb;
+          if (raise && !raise_early) rs *= kFixFactor;
+          l = l * alpha + rs;
+          m = m_new;
+          ms = ms_new;
+          if constexpr (kVariants) {
+            l_bar = l_bar * alpha + rs_bar;
+            cnt = c_new;
+            cnt_near = cn_new;
+            s2 = s2_new;
+            raised = raise;
+          }
+          tmem_st_wait();
+          tc_fence_before();
+          mbar_arrive(&p_full[t]);
+          continue;
+        }
         // near-tie mode: the largest score of the tile below its maximum
         float s2x = kNegInf;
         if (kVariants && p.near) {
@@ -844,7 +980,6 @@ __global__ void __launch_bounds__(384, 1)
         if (raise && !raise_early) rs *= kFixFactor;
         // rescale of the running O and l: exact, whenever the shift moves
         float alpha = ex2(ms - ms_new);
-        if (kWin && m == kNegInf) alpha = 0.f;   // nothing seen so far: ms is no shift, and O and l are 0
         if (raise != raised) alpha = raise ? alpha * kFixFactor : alpha / kFixFactor;
         l = l * alpha + rs;
         if (j > 0) {

@@ -35,10 +35,12 @@ int setup_device() {
     };
     auto both = [&](auto elem) {
       using E = decltype(elem);
-      setup(fa_fwd_kernel<64, false, E, true>, FwdLayout<64>::kAlloc, FwdLayout<64>::kLaunchRegs);
-      setup(fa_fwd_kernel<64, true, E, true>, FwdLayout<64>::kAlloc, FwdLayout<64>::kLaunchRegs);
-      setup(fa_fwd_kernel<128, false, E, true>, FwdLayout<128>::kAlloc, FwdLayout<128>::kLaunchRegs);
-      setup(fa_fwd_kernel<128, true, E, true>, FwdLayout<128>::kAlloc, FwdLayout<128>::kLaunchRegs);
+      setup(fa_fwd_kernel<64, false, E, 1>, FwdLayout<64>::kAlloc, FwdLayout<64>::kLaunchRegs);
+      setup(fa_fwd_kernel<64, true, E, 1>, FwdLayout<64>::kAlloc, FwdLayout<64>::kLaunchRegs);
+      setup(fa_fwd_kernel<64, false, E, 2>, FwdLayout<64>::kAlloc, FwdLayout<64>::kLaunchRegs);
+      setup(fa_fwd_kernel<128, false, E, 1>, FwdLayout<128>::kAlloc, FwdLayout<128>::kLaunchRegs);
+      setup(fa_fwd_kernel<128, true, E, 1>, FwdLayout<128>::kAlloc, FwdLayout<128>::kLaunchRegs);
+      setup(fa_fwd_kernel<128, false, E, 2>, FwdLayout<128>::kAlloc, FwdLayout<128>::kLaunchRegs);
       setup(fa_bwd_kernel<64, E, false, true>, BwdLayout<64>::kAlloc, BwdLayout<64>::kLaunchRegs);
       setup(fa_bwd_kernel<128, E, false, true>, BwdLayout<128>::kAlloc, BwdLayout<128>::kLaunchRegs);
     };
@@ -127,7 +129,9 @@ int window_fwd(const void* q, const void* k, const void* v, void* o, float* lse,
   p.window = window < N ? window : N;
   p.sinks = sinks < N ? sinks : N;
   const int n_items = p.n_pairs * p.BH;
-  auto kern = fix_mode == 1 ? fa_fwd_kernel<D, false, E, true> : fa_fwd_kernel<D, true, E, true>;
+  auto kern = fix_mode == 1  ? fa_fwd_kernel<D, false, E, 2>
+              : fix_mode == 0 ? fa_fwd_kernel<D, false, E, 1>
+                              : fa_fwd_kernel<D, true, E, 1>;
   return launch(kern, dim3(n_items < num_sms ? n_items : num_sms), dim3(L::kThreads), L::kAlloc, stream, mq, mk, mv,
                 mo, p) == cudaSuccess
              ? FA_OK
