@@ -72,12 +72,13 @@ struct DecLayout {
   static constexpr int kJoinCols = NB == 1 ? D : 64;
   static constexpr int kJoinRow = kJoinCols + 4;             // rows 4 banks apart: the warps' writes do not collide
   static_assert(4 * 8 * NB * kJoinRow * 4 <= 2 * kTileBytes, "the join does not fit a stage");
-  static constexpr int kMlOff = kStages * 2 * kTileBytes;    // [4 warps][8 NB] m and l
+  static constexpr int kMlOff = kStages * 2 * kTileBytes;    // [2][4 warps][8 NB] m and l
+  static constexpr int kMlFloats = 4 * 8 * NB * 2;
   // the queries of a unit, beside the stage of its first tile; 16 heads of 128
   // would cost the second CTA per SM and are read from global memory
   static constexpr bool kQSmem = !(NB == 2 && D == 128);
   static constexpr int kQBytes = kQSmem ? 8 * NB * D * 2 : 0;
-  static constexpr int kQOff = kMlOff + 4 * 8 * NB * 2 * 4;
+  static constexpr int kQOff = kMlOff + 2 * kMlFloats * 4;
   static constexpr int kBarOff = kQOff + kStages * kQBytes;
   static constexpr int kCumOff = kBarOff + 128;              // [S + 1] as DecodeParams::cum, then [S] lengths
   static constexpr int kThreads = 160;
@@ -194,7 +195,7 @@ __global__ void __launch_bounds__(160, 2)
   const float kNegInf = -__int_as_float(0x7f800000);
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-  float* ml = reinterpret_cast<float*>(smem + L::kMlOff);
+  float* ml_both = reinterpret_cast<float*>(smem + L::kMlOff);
   uint64_t* full = reinterpret_cast<uint64_t*>(smem + L::kBarOff);
   uint64_t* empty = full + L::kStages;
   volatile int* abort_flag = reinterpret_cast<volatile int*>(empty + L::kStages);
@@ -369,7 +370,7 @@ __global__ void __launch_bounds__(160, 2)
   const int row_k = warp * (16 * kRows) + (lane & 15);                          // K: rows of the four matrices
   const int row_v = warp * (16 * kRows) + (lane & 7) + ((lane >> 4) << 3);      // V: keys of the four matrices
 
-  int i = 0;                          // tiles taken
+  int i = 0, ends = 0;                // tiles taken; results joined
   for (int x = 0; x < n; ++x, w.next(cum, p.S, p.units)) {
     if (w.t == w.nt) continue;        // the place behind a unit
     int h0, nh;
@@ -521,7 +522,10 @@ __global__ void __launch_bounds__(160, 2)
       continue;
     }
 
-    // The unit's end, or the stretch's: the four warps' results are joined.
+    // The unit's end, or the stretch's: the four warps' results are joined.  m and
+    // l of one unit and the next lie apart, for a warp may come here again while
+    // another still reads them.
+    float* ml = ml_both + (ends++ & 1) * L::kMlFloats;
 #pragma unroll
     for (int nb = 0; nb < NB; ++nb)
 #pragma unroll
