@@ -16,7 +16,7 @@ ROOT = os.path.dirname(PKG)
 LIB = os.path.join(PKG, "libfa_b200.so")
 SOURCES = [os.path.join(PKG, "csrc", f) for f in ("fa_api.cu", "fa_cache.cu", "fa_window.cu")]
 HEADERS = [os.path.join(PKG, "csrc", f) for f in ("sm100.cuh", "fa_fwd.cuh", "fa_bwd.cuh", "fa_selftest.cuh",
-                                                  "fa_host.h", "fa_cache.cuh", "fa_decode.cuh")] + [
+                                                  "fa_host.h", "fa_cache.cuh", "fa_decode.cuh", "fa_window_pre.cuh")] + [
     os.path.join(ROOT, "include", f) for f in ("fa_b200.h", "fa_b200_cache.h", "fa_b200_window.h")]
 
 FAST_SOURCE = os.path.join(PKG, "csrc", "fast.cpp")

@@ -7,6 +7,7 @@
 #include "fa_bwd.cuh"
 #include "fa_fwd.cuh"
 #include "fa_host.h"
+#include "fa_window_pre.cuh"
 
 namespace fa {
 namespace {
@@ -156,8 +157,13 @@ int window_bwd(const void* q, const void* k, const void* v, const void* o, const
   float* near_part = reinterpret_cast<float*>(workspace + w.near);
   float* far_part = reinterpret_cast<float*>(workspace + w.far);
   const long long rows = (long long)BH * N;
-  if (launch(fa_bwd_pre_kernel<E>, dim3(unsigned((rows * 8 + 255) / 256)), dim3(256), 0, stream,
-             static_cast<const T*>(o), static_cast<const T*>(dout), dsum, dq_acc, rows, D) != cudaSuccess)
+  const float scale_log2 = float(double(scale) * 1.4426950408889634);
+  const int few = w.window + (long long)w.sinks <= kFewKeys || N < kFewKeys ? N : kFewKeys;
+  const unsigned few_blocks = unsigned(((long long)BH * few + 7) / 8);
+  const BwdPreParams pre{lse, dsum, dq_acc, rows, N, H, H / Hkv, w.window, w.sinks, few, few_blocks, scale_log2};
+  if (launch(fa_bwd_window_pre_kernel<D, E>, dim3(few_blocks + unsigned((rows * 8 + 255) / 256)), dim3(256), 0, stream,
+             static_cast<const T*>(o), static_cast<const T*>(dout), static_cast<const T*>(q),
+             static_cast<const T*>(k), static_cast<const T*>(v), pre) != cudaSuccess)
     return FA_ERR_LAUNCH;
   BwdWindowParams p{};
   p.lse = lse;
@@ -173,7 +179,7 @@ int window_bwd(const void* q, const void* k, const void* v, const void* o, const
   p.n_kv = (N + 127) / 128;
   p.causal = 1;
   p.scale = scale;
-  p.scale_log2 = float(double(scale) * 1.4426950408889634);
+  p.scale_log2 = scale_log2;
   p.after_pre = 1;
   p.window = w.window;
   p.sinks = w.sinks;

@@ -15,7 +15,9 @@ move it, from the arithmetic (h = half a step of the element format, eps / 2):
   subnormal step), and so is each gradient;
 * in the backward, P = exp(S - LSE) is off by 2 e_i (LSE carries e_i too) and is
   rounded for dV alone; dP is an FP32 sum like a score; D is taken from the
-  rounded O; dS is rounded: h |dS|, or 2^-25 absolute in fp16;
+  rounded O, or as the mean of dP weighted with P: off by what the weights and dP
+  are, and 2^-20 of the terms for the sums of up to 8 and the division; dS is
+  rounded: h |dS|, or 2^-25 absolute in fp16;
 * FP32 accumulation of up to some thousand terms adds less than 2^-18 of the
   terms' size.
 """
@@ -72,8 +74,9 @@ def forward(q, k, v, window, sinks, scale, eps):
     return o, lse, tol, tol_lse
 
 
-def backward(q, k, v, do, window, sinks, scale, eps):
-    """(dq, dk, dv) of sum(do * o), and (tol_dq, tol_dk, tol_dv)."""
+def backward(q, k, v, do, window, sinks, scale, eps, few=0):
+    """(dq, dk, dv) of sum(do * o), and (tol_dq, tol_dk, tol_dv); few: rows of up to
+    this many keys take D from their own P and dP."""
     q, k, v, do = _f64(q), _f64(k), _f64(v), _f64(do)
     B, H, N, d = q.shape
     g = H // k.shape[1]
@@ -88,7 +91,10 @@ def backward(q, k, v, do, window, sinks, scale, eps):
             dp, D = dd @ vv.T, (dd * o).sum(1, keepdims=True)
             ds = p * (dp - D)
             size = np.abs(dd) @ np.abs(vv).T
-            off = (p * (2.0 ** -23 * (d + 8) * size + (np.abs(dd) * tol_o).sum(1, keepdims=True)
+            off_d = (np.abs(dd) * tol_o).sum(1, keepdims=True)
+            own = p * (2.0 ** -23 * (d + 8) * size + 2 * err * (np.abs(dp) + np.abs(D)) + 2.0 ** -20 * np.abs(dp))
+            off_d = np.where(vis.sum(1, keepdims=True) <= few, own.sum(1, keepdims=True), off_d)
+            off = (p * (2.0 ** -23 * (d + 8) * size + off_d
                         + 2 * err * (np.abs(dp) + np.abs(D))))
             off = off + np.maximum(h * (np.abs(ds) + off), sub * vis) + 2.0 ** -18 * np.abs(ds)
             off_p = p * (h + 2 * err + 2.0 ** -18) + sub * vis

@@ -83,6 +83,21 @@ def test_window(fa, B, H, Hkv, N, d, window, sinks, dt):
     check(fa, draw(B, H, Hkv, N, d, dt, N + window), window, sinks)
 
 
+@pytest.mark.parametrize("B,H,Hkv,N,d,window,sinks,dt", [
+    (3, 2, 1, 1, 64, 7, 16, "bf16"), (2, 4, 2, 2, 128, 2, 1, "bf16"), (1, 3, 3, 3, 64, 8, 0, "fp16"), (4, 2, 2, 8, 64, 9, 0, "bf16"),
+    (2, 6, 2, 300, 64, 1, 0, "bf16"), (1, 2, 2, 700, 128, 5, 3, "bf16"), (2, 2, 1, 400, 128, 2, 6, "fp16"), (1, 4, 1, 500, 64, 1, 9, "bf16")])
+def test_gradients_of_rows_that_see_few_keys(fa, B, H, Hkv, N, d, window, sinks, dt):
+    """Rows of up to 8 keys have a D without O's rounding; one that sees a key alone has no gradient but dv."""
+    q, k, v, do = draw(B, H, Hkv, N, d, dt, N + d)
+    dev = [t.cuda() for t in (q, k, v, do)]
+    o, lse = fa.window.attention_window_fwd(*dev[:3], window, sinks)
+    grads = fa.window.attention_window_bwd(*dev[:3], o, lse, dev[3], window, sinks)
+    assert fa.fa_check_device_error() == 0
+    want, tol = window64.backward(q, k, v, do, window, sinks, d ** -0.5, torch.finfo(DT[dt]).eps, few=8)
+    for got, w, t, name in zip(grads, want, tol, ("dq", "dk", "dv")):
+        within(got, w, t, name)
+
+
 @pytest.mark.parametrize("fix", range(6))
 @pytest.mark.parametrize("d,dt", [(64, "bf16"), (128, "fp16")])
 def test_fix_modes_on_repeated_maxima(fa, fix, d, dt):
