@@ -80,16 +80,21 @@ BwdPlan bwd_plan(int B, int H, int Hkv, int N, int d, int window, int sinks) {
   const int far = pc.n_q - pc.near, sink_tiles = (w.sinks + 127) / 128;
   pc.split = sink_tiles < far ? sink_tiles : far;
   pc.far_rows = w.sinks < 128 * pc.split ? w.sinks : 128 * pc.split;
-  // steps of all items; a third of a CTA's share of them, four at least (an item
-  // loads K and V and writes its sums, about two steps' time)
+  // steps of all items; a third of a CTA's share of them, but four at least (an item
+  // loads K and V and writes its sums, about two steps' time), or where a CTA's
+  // share is smaller that, but two (8 heads over 2, N = 1024, d = 128, window 256:
+  // backward 27.9 us with four, 24.3 with two; 2 heads, N = 4096, d = 64, window 300:
+  // 20.0 and 19.4, with two in any case 25.2)
   const long long BHkv = (long long)B * Hkv;
   const long long near_steps = (long long)pc.n_q * pc.near - (long long)pc.near * (pc.near - 1) / 2;
   const long long far_steps = (long long)pc.split * far - (long long)pc.split * (pc.split - 1) / 2;
-  const long long share = ((near_steps + far_steps) * BHkv * pc.group + 3 * 148 - 1) / (3 * 148);
-  const long long item = share > 4 ? share : 4;
+  const long long steps = (near_steps + far_steps) * BHkv * pc.group;
+  const long long share = (steps + 3 * 148 - 1) / (3 * 148), whole = (steps + 147) / 148;
+  const int least = whole < 2 ? 2 : whole < 4 ? int(whole) : 4;
+  const long long item = share > least ? share : least;
   pc.near_parts = int(((long long)pc.near * pc.group + item - 1) / item);
   // far parts about as long as the others: every CTA takes as many items
-  const int part = pc.near * pc.group / pc.near_parts, far_item = part > 4 ? part : 4;
+  const int part = pc.near * pc.group / pc.near_parts, far_item = part > least ? part : least;
   const long long far_len = (long long)far * pc.group;
   pc.far_parts = !pc.split ? 0 : far_len < far_item ? 1 : int((far_len + far_item / 2) / far_item);
   pc.gaps = pc.near_parts > pc.group || (pc.split && pc.far_parts > (far - pc.split + 1) * pc.group);

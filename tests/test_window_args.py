@@ -86,10 +86,11 @@ def test_workspace_size(win):
     assert size(8, 12, 12, 1024, 64, 5000, 4) == base          # no query is past the window
     # 8 query tiles, 3 in a window, 5 behind it in one part beside the window's
     assert size(8, 12, 12, 1024, 64, 256, 4) == base + up(96 * 2 * 4 * 2 * 64 * 4)
-    # one head: its 3 tiles of 3, 2 and 1 steps fit the least length of a part
-    assert size(1, 1, 1, 300, 64, 256, 0) == up(300 * 64 * 4) + up(300 * 4)
-    # four heads over one: 12 steps a tile, in three parts of all rows
-    assert size(1, 4, 1, 300, 64, 256, 0) == up(1200 * 64 * 4) + up(1200 * 4) + up(3 * 300 * 2 * 64 * 4)
+    # one head: its tiles of 3, 2 and 1 steps in parts of two steps, the least length
+    assert size(1, 1, 1, 300, 64, 256, 0) == up(300 * 64 * 4) + up(300 * 4) + up(2 * 300 * 2 * 64 * 4)
+    assert size(1, 1, 1, 256, 64, 256, 0) == up(256 * 64 * 4) + up(256 * 4)
+    # four heads over one: 12 steps a tile, in six parts of all rows
+    assert size(1, 4, 1, 300, 64, 256, 0) == up(1200 * 64 * 4) + up(1200 * 4) + up(6 * 300 * 2 * 64 * 4)
     assert size(2, 4, 2, 1000, 64, 0, 4) == 0
     assert size(2, 4, 3, 1000, 64, 64, 4) == 0
     assert size(1, 1, 1, 1 << 20, 64, 10**12, 10**12) == size(1, 1, 1, 1 << 20, 64, 1 << 20, 1 << 20)
