@@ -195,6 +195,7 @@ struct BwdWindowParams : BwdParams {
   BwdPieces pc;
   float* near_part;     // [BH][near_parts][N][dK, dV][D], where near_parts > 1
   float* far_part;      // [BH][1 + far_parts][far_rows][dK, dV][D], where there are far parts
+  void* dq;             // [B*H, N, D] of the element type, where a query tile has one step
 };
 
 template <int D>
@@ -436,16 +437,18 @@ struct BwdSteps {
 // re-initialisation: `g` counts query-tile steps, `n_done` counts items.
 // E: the element format (ElemBF16 or ElemF16) of Q, K, V, dO, dK, dV and of
 // the P_bar and dS operands.  kPairs: the head-major pair schedule (BwdSched).
-// kWin: the windowed kernel (BwdWindow's items, and the window's mask).
-template <int D, typename E = ElemBF16, bool kPairs = false, bool kWin = false>
+// kWin: the windowed kernel (BwdWindow's items, and the window's mask); 2 where each
+// query tile has one step, whose dQ is written as it is.  (As a branch at run time
+// that cost the others 2 % at d = 64.)
+template <int D, typename E = ElemBF16, bool kPairs = false, int kWin = 0>
 __global__ void __launch_bounds__(512, 1)
     fa_bwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
                   const __grid_constant__ CUtensorMap tm_v, const __grid_constant__ CUtensorMap tm_do,
                   const __grid_constant__ CUtensorMap tm_dq, const __grid_constant__ CUtensorMap tm_dk,
                   const __grid_constant__ CUtensorMap tm_dv,
-                  const std::conditional_t<kWin, BwdWindowParams, BwdParams> p) {
+                  const std::conditional_t<kWin != 0, BwdWindowParams, BwdParams> p) {
   using L = BwdLayout<D>;
-  using Sched = std::conditional_t<kWin, BwdWindow<D>, BwdSched<kPairs>>;
+  using Sched = std::conditional_t<kWin != 0, BwdWindow<D>, BwdSched<kPairs>>;
   extern __shared__ __align__(1024) uint8_t smem[];
   uint64_t* bars = reinterpret_cast<uint64_t*>(smem + L::kBarOff);
   uint64_t* kv_full = bars;        // [2]
@@ -981,23 +984,38 @@ __global__ void __launch_bounds__(512, 1)
             tc_fence_before();
             mbar_arrive(dq_free);
           }
+          if constexpr (kWin == 2) {
+            if (sp.qt * 128 + rr < p.N) {
+              uint4* dst = reinterpret_cast<uint4*>(static_cast<typename E::T*>(p.dq) +
+                                                    (size_t(sp.bh_q) * p.N + sp.qt * 128 + rr) * D + c2 * 64);
 #pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            const int c = 2 * c2 + h;
-            uint8_t* box = stage + (box_seq & 1) * L::kStageBox;
-            if (lane == 0) bulk_wait_read<1>();        // the reduce issued from this box is done reading
-            __syncwarp();
-#pragma unroll
-            for (int c16 = 0; c16 < 8; ++c16)
-              *reinterpret_cast<uint4*>(box + lane * 128 + ((c16 ^ (lane & 7)) << 4)) =
-                  make_uint4(r[h][4 * c16], r[h][4 * c16 + 1], r[h][4 * c16 + 2], r[h][4 * c16 + 3]);
-            fence_proxy_async_smem();
-            __syncwarp();
-            if (lane == 0) {
-              tma_reduce_add_3d(&tm_dq, box, c * 32, sp.qt * 128 + wq * 32, sp.bh_q);
-              bulk_commit();
+              for (int i = 0; i < 8; ++i) {
+                const uint32_t* x = &r[i >> 2][8 * (i & 3)];
+                auto pair = [&](int at) {
+                  return E::pack(__uint_as_float(x[at]) * p.scale, __uint_as_float(x[at + 1]) * p.scale);
+                };
+                dst[i] = make_uint4(pair(0), pair(2), pair(4), pair(6));
+              }
             }
-            ++box_seq;
+          } else {
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+              const int c = 2 * c2 + h;
+              uint8_t* box = stage + (box_seq & 1) * L::kStageBox;
+              if (lane == 0) bulk_wait_read<1>();        // the reduce issued from this box is done reading
+              __syncwarp();
+#pragma unroll
+              for (int c16 = 0; c16 < 8; ++c16)
+                *reinterpret_cast<uint4*>(box + lane * 128 + ((c16 ^ (lane & 7)) << 4)) =
+                    make_uint4(r[h][4 * c16], r[h][4 * c16 + 1], r[h][4 * c16 + 2], r[h][4 * c16 + 3]);
+              fence_proxy_async_smem();
+              __syncwarp();
+              if (lane == 0) {
+                tma_reduce_add_3d(&tm_dq, box, c * 32, sp.qt * 128 + wq * 32, sp.bh_q);
+                bulk_commit();
+              }
+              ++box_seq;
+            }
           }
         }
       }

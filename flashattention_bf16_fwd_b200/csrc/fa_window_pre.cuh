@@ -23,7 +23,7 @@ constexpr int kFewKeys = 8;
 struct BwdPreParams {
   const float* lse;
   float* dsum;           // [BH, N]
-  float* dq_acc;         // [BH, N, D]
+  float* dq_acc;         // [BH, N, D], or nullptr where nothing is added to it
   long long rows;        // BH * N
   int N, H, group, window, sinks;
   int few;               // a row i sees min(i + 1, window + sinks) keys: the first `few` of each head see few
@@ -112,8 +112,7 @@ __global__ void __launch_bounds__(256) fa_bwd_window_pre_kernel(const typename E
     for (int c = 0; c < kWords; ++c) {
       od[c] = reinterpret_cast<const uint4*>(o + base)[c];
       dd[c] = reinterpret_cast<const uint4*>(dout + base)[c];
-      z[2 * c] = make_float4(0.f, 0.f, 0.f, 0.f);
-      z[2 * c + 1] = make_float4(0.f, 0.f, 0.f, 0.f);
+      if (p.dq_acc) z[2 * c] = z[2 * c + 1] = make_float4(0.f, 0.f, 0.f, 0.f);
     }
     sum = slice_dot<E>(od, dd);
   }

@@ -75,6 +75,9 @@ CASES = [  # B, H, Hkv, N, d, window, sinks, type
     (1, 8, 1, 700, 64, 300, 4, "bf16"),          # windows and far parts cut, some parts empty
     (1, 4, 1, 2500, 128, 600, 140, "bf16"),
     (1, 5, 1, 1300, 64, 400, 0, "fp16"),
+    (2, 8, 1, 100, 64, 30, 4, "bf16"),           # one query tile: dQ has one step, dK and dV are in parts
+    (3, 6, 2, 128, 128, 200, 0, "fp16"),
+    (1, 4, 4, 66, 128, 3, 2, "bf16"),
 ]
 
 
