@@ -62,6 +62,7 @@ struct FwdParams {
   int self_norm;        // divide O by the sum of the rounded P_bar instead of the unrounded P
   int near;             // detect near ties (P rounds to 1.0 in the element format) instead of exact ties of S
   int window, sinks;    // windowed kernel: key j is visible where j <= i and (i - j < window or j < sinks)
+  int item_log2;        // windowed kernel: an item has 2^item_log2 queries, 256 or 128 (then n_pairs counts those)
 };
 
 template <int D>
@@ -117,17 +118,17 @@ __device__ __forceinline__ int fwd_key_tile(const FwdItem& w, int j) { return j 
 
 __device__ __forceinline__ FwdItem fwd_window_item(const FwdParams& p, int item) {
   FwdItem it;
-  const int pair = p.n_pairs - 1 - item / p.BH;
   it.bh = item % p.BH;
-  it.q0_row = pair * 256;
-  const bool second = it.q0_row + 128 < p.N;
+  it.q0_row = (p.n_pairs - 1 - item / p.BH) << p.item_log2;
+  const int tile = it.q0_row >> 7;
+  const bool second = p.item_log2 == 8 && it.q0_row + 128 < p.N;
   const int a0 = max(0, it.q0_row - p.window + 1) >> 7;          // first tile of each query tile's window
   const int a1 = max(0, it.q0_row + 129 - p.window) >> 7;
-  const int last = 2 * pair + (second ? 1 : 0);                  // the last diagonal tile
+  const int last = tile + (second ? 1 : 0);                      // the last diagonal tile
   it.sink_tiles = min((min(p.sinks, p.N) + 127) >> 7, last + 1);
   it.gap = max(0, a0 - it.sink_tiles);
   it.nmax = last + 1 - it.gap;
-  it.n0 = 2 * pair + 1 - it.gap;
+  it.n0 = tile + 1 - it.gap;
   it.n1 = second ? it.nmax : 0;
   it.skip1 = (a1 > a0 && a0 >= it.sink_tiles) ? it.sink_tiles : -1;
   return it;

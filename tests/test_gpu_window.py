@@ -113,6 +113,22 @@ def test_fix_modes_on_repeated_maxima(fa, fix, d, dt):
     check(fa, x, 140, 3, fix=fix, bwd=False)
 
 
+@pytest.mark.parametrize("N,d,window,sinks,dt", [
+    (129, 64, 1, 0, "bf16"), (256, 128, 100, 3, "fp16"), (257, 64, 128, 0, "bf16"), (383, 128, 130, 140, "bf16"), (640, 64, 129, 4, "fp16"),
+    (777, 64, 191, 5, "bf16"), (900, 128, 257, 1, "fp16"), (1030, 64, 2000, 0, "bf16")])
+def test_many_heads_are_as_few(fa, N, d, window, sinks, dt):
+    """With more query tiles than CTAs two share one, or follow one another in it; the bits are those of a call with
+    few heads, where each has its own."""
+    q, k, v, _ = (t.cuda() for t in draw(2, 150, 75, N, d, dt, N))
+    for fix in range(6):
+        o, lse = fa.window.attention_window_fwd(q, k, v, window, sinks, fix_mode=fix)
+        for b, h in ((0, 0), (0, 77), (1, 40), (1, 149)):
+            few = fa.window.attention_window_fwd(q[b:b + 1, h:h + 1].contiguous(), k[b:b + 1, h // 2:h // 2 + 1].contiguous(),
+                                                 v[b:b + 1, h // 2:h // 2 + 1].contiguous(), window, sinks, fix_mode=fix)
+            assert torch.equal(o[b, h], few[0][0, 0]) and torch.equal(lse[b, h], few[1][0, 0]), (fix, b, h)
+    assert fa.fa_check_device_error() == 0
+
+
 def test_window_as_wide_as_the_sequence_is_causal_attention(fa):
     """The same tiles in the same order: the bits are those of attention_fwd in the modes that share its softmax."""
     for d, N in ((64, 900), (128, 777)):
