@@ -102,14 +102,16 @@ struct FastDiv {
 struct BwdPieces {
   int n_q, near, group;
   int near_parts;       // parts of a key tile's window steps
-  int split, far_parts; // key tiles with a far part; its parts
+  int split, far_parts; // key tiles with a far part of its own; its parts
   int far_rows;         // sink rows in them
+  int far_from;         // a far item begins `near` query tiles on, or (split = 0) with the window
+  int near_first;       // the first key tile that has window items: those before it are whole far items
   bool gaps;            // some parts are empty
   FastDiv by_heads, by_tiles, by_near, by_far;   // by BH, n_q, near_parts, far_parts
   // query tiles of key tile kv's window (far = false) or of its far part
   __host__ __device__ __forceinline__ int tiles(bool far, int kv) const {
     const int left = n_q - kv;
-    return far ? left - near : left < near ? left : near;
+    return far ? left - far_from : left < near ? left : near;
   }
   // Part c has the steps from c * (steps / parts) + min(c, steps % parts) on: none
   // where there are fewer steps than parts and c is not below them.
@@ -317,17 +319,18 @@ struct BwdSched {
 // The windowed kernel's items: the parts of BwdPieces.  A tile with sinks as one
 // item would take N / 128 steps where the others take `near`, and few heads with
 // a wide window give fewer items than SMs; so both are cut, into items of about
-// the same length (every CTA takes as many), four steps at least (H = 4 over one
+// the same length (every CTA takes as many), see bwd_plan() (H = 4 over one
 // K/V head, N = 2048, d = 128, window 1024: 107 us uncut, 36 us).  Parts leave
 // FP32 dK and dV, which fa_bwd_window_finish_kernel adds in a fixed order; a
-// window in one part writes its final rows itself.  The far parts come first,
+// window in one part writes its final rows itself, and where a CTA takes many items
+// a far part goes with it.  The far parts come first,
 // then the key tiles, head by head: neighbours share their queries in the L2.
 template <int D>
 struct BwdWindow {
   int rnd, item, n_far, n_items;
   __device__ __forceinline__ explicit BwdWindow(const BwdWindowParams& p) : rnd(0), item(snake_item(0)) {
-    n_far = p.pc.split * p.pc.far_parts * p.BH;
-    n_items = n_far + p.n_kv * p.pc.near_parts * p.BH;
+    n_far = (p.pc.split + p.pc.near_first) * p.pc.far_parts * p.BH;
+    n_items = n_far + (p.n_kv - p.pc.near_first) * p.pc.near_parts * p.BH;
     skip(p);
   }
   __device__ __forceinline__ bool valid() const { return item < n_items; }
@@ -345,7 +348,7 @@ struct BwdWindow {
       const int n = item - n_far, i = p.pc.by_near.div(n);
       c = n - i * p.pc.near_parts;
       bh = p.pc.by_tiles.div(i);
-      kv = i - bh * p.n_kv;
+      kv = i - bh * (p.n_kv - p.pc.near_first) + p.pc.near_first;
     }
   }
   // a tile with fewer steps than parts has empty ones
@@ -369,7 +372,7 @@ struct BwdWindow {
     int c;
     where(p, far, w.bh, w.kv_tile, c);
     w.key0 = w.kv_tile * 128;
-    w.i_start = w.kv_tile + (far ? p.pc.near : 0);
+    w.i_start = w.kv_tile + (far ? p.pc.far_from : 0);
     w.n_it_head = p.pc.tiles(far, w.kv_tile);
     w.n_it = w.n_it_head * p.group;
     w.step0 = 0;
@@ -383,7 +386,7 @@ struct BwdWindow {
     w.part_rows = 0;
     w.direct = !far;
     const long long bh = w.bh;
-    if (far || (p.pc.near_parts == 1 && w.kv_tile < p.pc.split)) {
+    if ((far && p.pc.split) || (p.pc.near_parts == 1 && w.kv_tile < p.pc.split)) {
       w.part_rows = p.pc.far_rows;
       w.part = p.far_part + (bh * (1 + p.pc.far_parts) + (far ? 1 + c : 0)) * p.pc.far_rows * (2 * D);
     } else if (p.pc.near_parts > 1) {

@@ -129,6 +129,28 @@ def test_many_heads_are_as_few(fa, N, d, window, sinks, dt):
     assert fa.fa_check_device_error() == 0
 
 
+@pytest.mark.parametrize("B,H,Hkv,N,d,window,sinks,dt", [
+    (8, 12, 12, 900, 64, 200, 4, "bf16"), (6, 48, 24, 650, 128, 100, 140, "fp16"), (4, 64, 32, 1024, 64, 3, 260, "bf16")])
+def test_backward_of_many_heads(fa, B, H, Hkv, N, d, window, sinks, dt):
+    """Enough heads that the sinks' queries behind the window go with those in it: some heads against the oracle, and
+    dk and dv the same bits again."""
+    q, k, v, do = draw(B, H, Hkv, N, d, dt, N)
+    dev = [t.cuda() for t in (q, k, v, do)]
+    o, lse = fa.window.attention_window_fwd(*dev[:3], window, sinks)
+    grads = fa.window.attention_window_bwd(*dev[:3], o, lse, dev[3], window, sinks)
+    assert fa.fa_check_device_error() == 0
+    again = fa.window.attention_window_bwd(*dev[:3], o, lse, dev[3], window, sinks)
+    assert torch.equal(grads[1], again[1]) and torch.equal(grads[2], again[2])
+    g, eps = H // Hkv, torch.finfo(DT[dt]).eps
+    for b, x in ((0, 0), (B - 1, Hkv - 1), (B // 2, Hkv // 2)):
+        hs = slice(x * g, x * g + g)
+        want, tol = window64.backward(q[b:b + 1, hs], k[b:b + 1, x:x + 1], v[b:b + 1, x:x + 1], do[b:b + 1, hs], window, sinks,
+                                      d ** -0.5, eps)
+        for got, w, t, name in zip((grads[0][b:b + 1, hs], grads[1][b:b + 1, x:x + 1], grads[2][b:b + 1, x:x + 1]), want, tol,
+                                   ("dq", "dk", "dv")):
+            within(got, w, t, name)
+
+
 def test_window_as_wide_as_the_sequence_is_causal_attention(fa):
     """The same tiles in the same order: the bits are those of attention_fwd in the modes that share its softmax."""
     for d, N in ((64, 900), (128, 777)):

@@ -84,8 +84,11 @@ def test_workspace_size(win):
     base = up(rows * 64 * 4) + up(rows * 4)
     assert size(8, 12, 12, 1024, 64, 256, 0) == base
     assert size(8, 12, 12, 1024, 64, 5000, 4) == base          # no query is past the window
-    # 8 query tiles, 3 in a window, 5 behind it in one part beside the window's
-    assert size(8, 12, 12, 1024, 64, 256, 4) == base + up(96 * 2 * 4 * 2 * 64 * 4)
+    # 8 query tiles, 3 in a window, 5 behind it, the same item; with half the heads a part beside the window's
+    assert size(8, 12, 12, 1024, 64, 256, 4) == base
+    assert size(4, 12, 12, 1024, 64, 256, 4) == base // 2 + up(48 * 2 * 4 * 2 * 64 * 4)
+    # 16 query tiles, 2 in a window, 14 behind it in four parts
+    assert size(8, 12, 12, 2048, 64, 128, 4) == 2 * base + up(96 * 5 * 4 * 2 * 64 * 4)
     # one head: its tiles of 3, 2 and 1 steps in parts of two steps, the least length
     assert size(1, 1, 1, 300, 64, 256, 0) == up(300 * 64 * 4) + up(300 * 4) + up(2 * 300 * 2 * 64 * 4)
     assert size(1, 1, 1, 256, 64, 256, 0) == up(256 * 64 * 4) + up(256 * 4)
