@@ -42,7 +42,7 @@ FA_API int fa_window_fwd(const void* q, const void* k, const void* v, void* o, f
  *   workspace : device scratch, >= fa_window_bwd_workspace_size() bytes,
  *       16-byte aligned, contents on entry ignored; calls that may run at the
  *       same time need one each.  It holds the FP32 dQ accumulator and D of
- *       fa_bwd, and FP32 pieces of the sinks' dK and dV.
+ *       fa_bwd, and FP32 pieces of dK and dV that several CTAs sum.
  * D, the row sums of dO * O, is taken from the rounded o; in rows that see up to
  * 8 keys (the first 8 tokens, and every one where window + sinks <= 8) it is
  * recomputed from q, k, v and lse, where the rounding of o would be the largest
