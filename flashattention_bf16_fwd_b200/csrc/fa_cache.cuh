@@ -185,7 +185,10 @@ __device__ __forceinline__ int count_pages(const CacheParams& p, bool used, int*
   return total;
 }
 
-__device__ __forceinline__ int pages_of(const CacheParams& p, int len) { return (len + p.page - 1) / p.page; }
+// Pages that hold len >= 0 tokens.  (The sum may pass 2^31 where a table's row has room for nearly that many.)
+__device__ __forceinline__ int pages_of(const CacheParams& p, int len) {
+  return int((unsigned(len) + unsigned(p.page - 1)) / unsigned(p.page));
+}
 
 // The request that page `rank` belongs to, where need[i] pages are wanted before
 // request i: the last i with need[i] <= rank (several may begin at one rank; the

@@ -91,9 +91,10 @@ struct DecLayout {
 };
 
 // The tiles of a sequence: those with a sink, then those of the window (all
-// keys where nothing is hidden).
+// keys where nothing is hidden).  Keys are counted without a sign: a table's row
+// may have room for 2^31 - 8 tokens, and the last tile then ends past 2^31.
 struct DecSpan {
-  int n, lo, sk;    // visible: key < n and (key >= lo or key < sk)
+  unsigned n, lo, sk;    // visible: key < n and (key >= lo or key < sk)
   int st, skip;     // tiles before the gap; tiles in the gap
   int nt;           // tiles
 };
@@ -101,19 +102,20 @@ struct DecSpan {
 template <int kTile>
 __device__ __forceinline__ DecSpan dec_span(const DecodeParams& p, int len) {
   DecSpan s;
-  s.n = min(max(len, 0), p.M * p.page);
-  s.lo = p.window > 0 ? max(0, s.n - p.window) : 0;
-  s.sk = min(p.sinks, s.n);
-  const int all = (s.n + kTile - 1) / kTile;
-  s.st = min((s.sk + kTile - 1) / kTile, all);
-  s.skip = max(0, s.lo / kTile - s.st);
+  const int n = min(max(len, 0), p.M * p.page);
+  s.n = n;
+  s.lo = p.window > 0 ? max(0, n - p.window) : 0;
+  s.sk = min(p.sinks, n);
+  const int all = int((s.n + kTile - 1) / kTile);
+  s.st = int((s.sk + kTile - 1) / kTile);
+  s.skip = max(0, int(s.lo / kTile) - s.st);
   s.nt = all - s.skip;
   return s;
 }
 
 template <int kTile>
-__device__ __forceinline__ int dec_key0(const DecSpan& s, int t) {
-  return (t < s.st ? t : t + s.skip) * kTile;
+__device__ __forceinline__ unsigned dec_key0(const DecSpan& s, int t) {
+  return unsigned(t < s.st ? t : t + s.skip) * kTile;
 }
 
 // First place of CTA c's stretch when T places are divided among G CTAs.
@@ -301,11 +303,11 @@ __global__ void __launch_bounds__(160, 2)
       real = u.t < u.nt;
       if (!real) return;
       const DecSpan sp = dec_span<kTile>(p, lens[u.s]);
-      const int key = dec_key0<kTile>(sp, u.t) + my_box * p.box;
-      row = key % p.page;
+      const unsigned key = dec_key0<kTile>(sp, u.t) + unsigned(my_box * p.box);
+      row = int(key % unsigned(p.page));
       head = u.unit / p.blocks;
       seen = key < sp.n && (key + p.box > sp.lo || key < sp.sk);
-      if (seen) id = p.table[size_t(u.s) * p.M + key / p.page];       // not looked at before its batch's turn
+      if (seen) id = p.table[size_t(u.s) * p.M + key / unsigned(p.page)];   // not looked at before its batch's turn
       if (L::kQSmem && my_box == 0 && (i == 0 || u.t == 0)) {          // the unit's first tile here
         int h0, nh;
         heads(u, h0, nh);
@@ -404,8 +406,8 @@ __global__ void __launch_bounds__(160, 2)
       }
       fresh = false;
     }
-    auto seen = [&](int key) { return key < sp.n && (key >= sp.lo || key < sp.sk); };
-    const int kw = dec_key0<kTile>(sp, w.t) + warp * (16 * kRows);      // this warp's first key
+    auto seen = [&](unsigned key) { return key < sp.n && (key >= sp.lo || key < sp.sk); };
+    const unsigned kw = dec_key0<kTile>(sp, w.t) + unsigned(warp * (16 * kRows));   // this warp's first key
     const bool whole = kw + 16 * kRows <= sp.n && (kw >= sp.lo || kw + 16 * kRows <= sp.sk);
     const bool none = kw >= sp.n || (kw >= sp.sk && kw + 16 * kRows <= sp.lo);
     if (ok && !none) {
@@ -493,7 +495,7 @@ __global__ void __launch_bounds__(160, 2)
         // need not be 0
         uint32_t keep0 = 0xffffffffu, keep1 = 0xffffffffu;
         if (!whole) {
-          const int kk = kw + 16 * r + tq * 2;
+          const unsigned kk = kw + 16 * r + tq * 2;
           keep0 = (seen(kk) ? 0xffffu : 0u) | (seen(kk + 1) ? 0xffff0000u : 0u);
           keep1 = (seen(kk + 8) ? 0xffffu : 0u) | (seen(kk + 9) ? 0xffff0000u : 0u);
         }
