@@ -396,7 +396,8 @@ __global__ void __launch_bounds__(256) fa_cache_free_kernel(const CacheParams p,
 }
 
 // compact, first kernel: one CTA.  Writes the moves (source pages, and their
-// destinations) and which move each source page is; counts move with the pages.
+// destinations) and which move each of those pages belongs to; counts move with
+// the pages.
 // With u(x) pages in use before page x, a free page x < live is the destination
 // number x - u(x), and a used page x >= live the source number u(x) - u(live).
 __global__ void __launch_bounds__(kPlanThreads) fa_cache_compact_plan_kernel(const CacheParams p, int32_t* live_out,
@@ -421,7 +422,10 @@ __global__ void __launch_bounds__(kPlanThreads) fa_cache_compact_plan_kernel(con
     for (int i = 0; i < kPer; ++i) {
       const int x = q.first + i;
       const bool in_use = q.used_bits >> i & 1u;
-      if (x < live && !in_use) to[x - u] = x;      // (live <= P)
+      if (x < live && !in_use) {                   // (live <= P)
+        to[x - u] = x;
+        went[x] = x - u;
+      }
       if (x >= live && in_use) {
         from[u - u_live] = x;
         went[x] = u - u_live;
@@ -452,16 +456,22 @@ __global__ void __launch_bounds__(256) fa_cache_compact_copy_kernel(const CacheP
   const int n = *moves, first = *live;
   const long long entries = (long long)p.S * p.M;
   for (long long i = (long long)blockIdx.x * 256 + threadIdx.x; i < entries; i += (long long)gridDim.x * 256) {
-    const int s = int(i / p.M);
-    if (int(i % p.M) >= pages_of(p, cache_len(p, p.lens[s]))) continue;
+    const int s = int(i / p.M), at = int(i % p.M), len = p.lens[s];
+    if (at >= pages_of(p, cache_len(p, len))) continue;
     const int id = p.table[i];
-    if (id < first && id >= 0) continue;
-    // a page past the pages in use moved, unless the table names a free page
-    const int m = id >= 0 && id < p.P ? went[id] : -1;
-    if (m >= 0 && m < n && from[m] == id)
+    // the move of a page that has one (of others `went` says nothing, and what it
+    // holds is checked against the moves)
+    const int m = n > 0 && id >= 0 && id < p.P ? went[id] : -1;
+    const bool moves_here = m >= 0 && m < n;
+    if (id >= 0 && id < first) {
+      if (!(moves_here && to[m] == id)) continue;  // a page in use that stays
+    } else if (moves_here && from[m] == id) {
       p.table[i] = to[m];
-    else
-      cache_error(p);
+      continue;
+    }
+    // no page, or a free one: the number may be another page's by now, or soon
+    p.table[i] = -1;
+    cache_error(p);
   }
   // A group of threads has four words each under way: the CTA where a page is 16 KB
   // or more (8 layers of 32 KB pages: 158 us, warp by warp 161), a warp where it is
