@@ -457,6 +457,7 @@ __global__ void __launch_bounds__(256) fa_cache_compact_copy_kernel(const CacheP
   const long long entries = (long long)p.S * p.M;
   for (long long i = (long long)blockIdx.x * 256 + threadIdx.x; i < entries; i += (long long)gridDim.x * 256) {
     const int s = int(i / p.M), at = int(i % p.M), len = p.lens[s];
+    if (at == 0 && !cache_len_ok(p, len)) cache_error(p);
     if (at >= pages_of(p, cache_len(p, len))) continue;
     const int id = p.table[i];
     // the move of a page that has one (of others `went` says nothing, and what it

@@ -138,7 +138,9 @@ FA_API int fa_cache_free(int32_t* refs, int32_t* table, int32_t* lens, const int
  * to the k-th free page below live, in all layers, and tables and counts
  * follow.  The pages from live on are then free, and their contents unchanged.
  * An entry in use that names a free page, or a number out of range, becomes -1
- * (a page that moves could take its place) and is reported.
+ * (a page that moves could take its place) and is reported.  A length out of
+ * range counts as the nearest in range, here and in fa_cache_free, and is
+ * reported.
  *   live out  : int32 [1], device: the number of pages in use.
  *   workspace : fa_cache_workspace_size(S, P) bytes, as in fa_decode.
  */

@@ -59,6 +59,17 @@ def test_compact_with_nothing_to_move(fa):
     assert fa.fa_check_device_error() == 0 and table.tolist() == [[1, 0, 5]]
 
 
+@pytest.mark.parametrize("length,row", [(-1, [6, 5]), (-2**31, [6, 5]), (17, [0, 1]), (2**31 - 1, [0, 1])])
+def test_compact_reports_lengths_out_of_range(fa, length, row):
+    """They count as the nearest in range."""
+    kp, vp = pools(1, 8)
+    refs, table, lens = counts(8, [6, 5]), i32([[6, 5], [7, 7]]), i32([length, 0])
+    assert fa.cache.cache_compact(kp, vp, refs, table, lens).item() == 2
+    assert fa.fa_check_device_error() == FA_ERR_PAGES
+    want = {6: 1, 5: 0}
+    assert table.tolist() == [[want[6], want[5]] if length > 0 else row, [7, 7]] and lens.tolist() == [length, 0]
+
+
 def test_fork_of_a_full_page_out_of_range(fa):
     kp, vp = pools(1, 6)
     refs, table, lens = counts(6, [1, 3]), i32([[1, 6, 3], [-1] * 3]), i32([20, 0])
