@@ -271,7 +271,8 @@ __global__ void __launch_bounds__(kPlanThreads) fa_cache_reserve_kernel(const Ca
 }
 
 // One fork: dst takes `whole` shared pages of src and, if rest > 0, page `to`
-// with the first `rest` tokens of page `from`.
+// with the first `rest` tokens of page `from`.  A `from` that is no page stands in
+// dst's row itself, and there is no `to`.
 struct ForkPlan {
   int src, dst, whole, rest, from, to;
 };
@@ -299,8 +300,10 @@ __global__ void __launch_bounds__(kPlanThreads) fa_cache_fork_plan_kernel(const 
       ok &= !(atomicOr(&taken[b >> 5], 1u << (b & 31)) >> (b & 31) & 1u);
     }
     bad |= !ok;
+    const int from = ok && n % p.page ? p.table[size_t(a) * p.M + n / p.page] : -1;
+    plan[f].from = from;
     len[f] = n;
-    need[f] = ok && n % p.page != 0;
+    need[f] = from >= 0 && from < p.P;
   }
   if (__syncthreads_or(bad)) {
     if (threadIdx.x == 0) {
@@ -318,12 +321,12 @@ __global__ void __launch_bounds__(kPlanThreads) fa_cache_fork_plan_kernel(const 
   if (threadIdx.x == 0) *missing = lacking;
   if (lacking) return;
   for (int f = threadIdx.x; f < F; f += kPlanThreads) {
-    ForkPlan* e = plan + f;                        // `to` is written above
+    ForkPlan* e = plan + f;                        // `from` and `to` are written above
     e->src = src[f];
     e->dst = dst[f];
     e->whole = len[f] / p.page;
     e->rest = len[f] % p.page;
-    e->from = e->rest ? p.table[size_t(e->src) * p.M + e->whole] : -1;
+    if (e->rest && (e->from < 0 || e->from >= p.P)) p.table[size_t(e->dst) * p.M + e->whole] = e->from;
     p.lens[e->dst] = len[f];
   }
   if (threadIdx.x == 0) *plan_n = F;

@@ -70,6 +70,23 @@ def test_compact_reports_lengths_out_of_range(fa, length, row):
     assert table.tolist() == [[want[6], want[5]] if length > 0 else row, [7, 7]] and lens.tolist() == [length, 0]
 
 
+@pytest.mark.parametrize("bad", [10, -1, 2**31 - 1, -2**31])
+def test_fork_of_a_last_page_out_of_range(fa, bad):
+    """The number is copied as it is: no page is taken for it, and none is missing."""
+    kp, vp = pools(2, 10)
+    refs = counts(10, [4, 2, 7])
+    table, lens = i32([[4, bad, -1], [2, 7, -1], [-1] * 3, [-1] * 3, [-1] * 3]), i32([12, 11, 0, 0, 0])
+    refs[torch.tensor([0, 1, 3, 5, 6])] = 1             # two pages are free, for the two forks of sequence 1
+    missing = fa.cache.cache_fork(kp, vp, refs, table, lens, i32([1, 0, 1]), i32([2, 3, 4]))
+    assert missing.item() == 0 and fa.fa_check_device_error() == FA_ERR_PAGES
+    assert table.tolist() == [[4, bad, -1], [2, 7, -1], [2, 8, -1], [4, bad, -1], [2, 9, -1]]
+    assert refs.tolist() == [1, 1, 3, 1, 2, 1, 1, 1, 1, 1] and lens.tolist() == [12, 11, 11, 12, 11]
+    for layer in range(2):
+        for new in (8, 9):
+            assert kp[layer, new, 0, :, 0].tolist() == [10 * layer + 7] * 3 + [10 * layer + new] * 5
+            assert vp[layer, new, 0, :, 0].tolist() == [-10 * layer - 7] * 3 + [-10 * layer - new] * 5
+
+
 def test_fork_of_a_full_page_out_of_range(fa):
     kp, vp = pools(1, 6)
     refs, table, lens = counts(6, [1, 3]), i32([[1, 6, 3], [-1] * 3]), i32([20, 0])
