@@ -5,8 +5,9 @@
 // does the same in one step for the common call: tensors of the right shapes on
 // the current device, the current stream, a workspace of its own.  It returns
 // None without having done anything where a call is not that, or where the
-// library refuses it; window.py and cache.py then take their own way, which
-// says what is wrong.  Host time of a call by that way and by this: windowed
+// library refuses its arguments; window.py and cache.py then take their own way,
+// which says what is wrong.  A failed launch is raised here and not tried again:
+// part of the call may have run.  Host time of a call by that way and by this: windowed
 // forward 13.1 and 4.9 us, backward 22.4 and 10.9, decoding 18.5 and 7.6, append
 // 8.1 and 2.9, reserve 8.4 and 3.2, fork 15.6 and 6.3.
 #include <Python.h>
@@ -102,6 +103,18 @@ PyObject* tuple_of(const T&... t) {
   return r;
 }
 
+// What a call that did not return FA_OK leads to.  Only a launch can fail after
+// something has been launched; the other statuses are refusals before that.  (A
+// second compaction after one whose copy was not launched would find the counts
+// moved and nothing left to do.)
+PyObject* not_ok(const char* call, int status) {
+  if (status != FA_ERR_LAUNCH) Py_RETURN_NONE;
+  PyObject* fa = PyImport_ImportModule("flashattention_bf16_fwd_b200.fa");
+  PyObject* r = fa ? PyObject_CallMethod(fa, "_check", "si", call, status) : nullptr;   // raises
+  Py_XDECREF(fa);
+  return r;
+}
+
 #define FA_IF(condition) \
   if (!(condition)) Py_RETURN_NONE
 
@@ -131,9 +144,10 @@ PyObject* window_fwd(PyObject*, PyObject* const* a, Py_ssize_t n) {
         get_scale(a[5], h.q->size(3), scale) && get_int(a[6], fix_mode));
   const auto s = h.q->sizes();
   const Tensor o = empty(s, h.q->scalar_type(), *h.q), lse = empty(s.slice(0, 3), at::kFloat, *h.q);
-  FA_IF(fa_window_fwd(h.q->data_ptr(), h.k->data_ptr(), h.v->data_ptr(), o.data_ptr(), lse.data_ptr<float>(), int(s[0]),
-                      int(s[1]), int(h.k->size(1)), int(s[2]), int(s[3]), window, sinks, scale, fix_mode, h.elem,
-                      stream_of(*h.q)) == FA_OK);
+  const int status = fa_window_fwd(h.q->data_ptr(), h.k->data_ptr(), h.v->data_ptr(), o.data_ptr(),
+                                   lse.data_ptr<float>(), int(s[0]), int(s[1]), int(h.k->size(1)), int(s[2]),
+                                   int(s[3]), window, sinks, scale, fix_mode, h.elem, stream_of(*h.q));
+  if (status) return not_ok("fa_window_fwd", status);
   return tuple_of(o, lse);
   END_HANDLE_TH_ERRORS
 }
@@ -155,10 +169,11 @@ PyObject* window_bwd(PyObject*, PyObject* const* a, Py_ssize_t n) {
   FA_IF(need);
   const Tensor dq = empty(s, h.q->scalar_type(), *h.q), dk = empty(h.k->sizes(), h.q->scalar_type(), *h.q),
                dv = empty(h.k->sizes(), h.q->scalar_type(), *h.q), ws = bytes(need, *h.q);
-  FA_IF(fa_window_bwd(h.q->data_ptr(), h.k->data_ptr(), h.v->data_ptr(), o->data_ptr(),
-                      static_cast<const float*>(lse->data_ptr()), dout->data_ptr(), dq.data_ptr(), dk.data_ptr(),
-                      dv.data_ptr(), ws.data_ptr(), need, B, H, Hkv, N, d, window, sinks, scale, h.elem,
-                      stream_of(*h.q)) == FA_OK);
+  const int status = fa_window_bwd(h.q->data_ptr(), h.k->data_ptr(), h.v->data_ptr(), o->data_ptr(),
+                                   static_cast<const float*>(lse->data_ptr()), dout->data_ptr(), dq.data_ptr(),
+                                   dk.data_ptr(), dv.data_ptr(), ws.data_ptr(), need, B, H, Hkv, N, d, window, sinks,
+                                   scale, h.elem, stream_of(*h.q));
+  if (status) return not_ok("fa_window_bwd", status);
   return tuple_of(dq, dk, dv);
   END_HANDLE_TH_ERRORS
 }
@@ -218,9 +233,10 @@ PyObject* decode(PyObject*, PyObject* const* a, Py_ssize_t n) {
   const size_t need = fa_decode_workspace_size(S, H, Hkv, d);
   FA_IF(need);
   const Tensor o = empty({S, H, d}, q->scalar_type(), *q), lse = empty({S, H}, at::kFloat, *q), ws = bytes(need, *q);
-  FA_IF(fa_decode(q->data_ptr(), c.k->data_ptr(), c.v->data_ptr(), ints(c.table), ints(c.lens), o.data_ptr(),
-                  lse.data_ptr<float>(), ws.data_ptr(), need, S, H, Hkv, d, int(c.P), int(c.page), int(c.M), stride,
-                  window, sinks, scale, c.elem, stream_of(*q)) == FA_OK);
+  const int status = fa_decode(q->data_ptr(), c.k->data_ptr(), c.v->data_ptr(), ints(c.table), ints(c.lens),
+                               o.data_ptr(), lse.data_ptr<float>(), ws.data_ptr(), need, S, H, Hkv, d, int(c.P),
+                               int(c.page), int(c.M), stride, window, sinks, scale, c.elem, stream_of(*q));
+  if (status) return not_ok("fa_decode", status);
   return tuple_of(o, lse);
   END_HANDLE_TH_ERRORS
 }
@@ -237,9 +253,10 @@ PyObject* append(PyObject*, PyObject* const* a, Py_ssize_t n) {
     cu = dense_int(a[6], 1);
     FA_IF(cu && cu->size(0) == c.S + 1);
   }
-  FA_IF(fa_cache_append(k->data_ptr(), v->data_ptr(), c.k->data_ptr(), c.v->data_ptr(), ints(c.table), ints(c.lens),
-                        cu ? ints(cu) : nullptr, int(k->size(0)), int(c.S), int(c.Hkv), int(c.d), int(c.P), int(c.page),
-                        int(c.M), ks, vs, stream_of(*c.k)) == FA_OK);
+  const int status = fa_cache_append(k->data_ptr(), v->data_ptr(), c.k->data_ptr(), c.v->data_ptr(), ints(c.table),
+                                     ints(c.lens), cu ? ints(cu) : nullptr, int(k->size(0)), int(c.S), int(c.Hkv),
+                                     int(c.d), int(c.P), int(c.page), int(c.M), ks, vs, stream_of(*c.k));
+  if (status) return not_ok("fa_cache_append", status);
   Py_RETURN_TRUE;
   END_HANDLE_TH_ERRORS
 }
@@ -258,8 +275,9 @@ PyObject* reserve(PyObject*, PyObject* const* a, Py_ssize_t n) {
   const Tensor* add = dense_int(a[3], 1);
   FA_IF(add && add->size(0) == c.S);
   const Tensor missing = empty({1}, at::kInt, *c.refs);
-  FA_IF(fa_cache_reserve(ints(c.refs), ints(c.table), ints(c.lens), ints(add), ints(&missing), int(c.S),
-                         int(c.refs->size(0)), page, int(c.M), stream_of(*c.refs)) == FA_OK);
+  const int status = fa_cache_reserve(ints(c.refs), ints(c.table), ints(c.lens), ints(add), ints(&missing), int(c.S),
+                                      int(c.refs->size(0)), page, int(c.M), stream_of(*c.refs));
+  if (status) return not_ok("fa_cache_reserve", status);
   return THPVariable_Wrap(missing);
   END_HANDLE_TH_ERRORS
 }
@@ -275,9 +293,11 @@ PyObject* fork(PyObject*, PyObject* const* a, Py_ssize_t n) {
   const size_t need = fa_cache_workspace_size(int(c.S), int(c.P));
   FA_IF(need);
   const Tensor missing = empty({1}, at::kInt, *c.refs), ws = bytes(need, *c.refs);
-  FA_IF(fa_cache_fork(c.k->data_ptr(), c.v->data_ptr(), ints(c.refs), ints(c.table), ints(c.lens), ints(src), ints(dst),
-                      ints(&missing), ws.data_ptr(), need, int(src->size(0)), int(c.L), int(c.S), int(c.Hkv), int(c.d),
-                      int(c.P), int(c.page), int(c.M), stream_of(*c.refs)) == FA_OK);
+  const int status = fa_cache_fork(c.k->data_ptr(), c.v->data_ptr(), ints(c.refs), ints(c.table), ints(c.lens),
+                                   ints(src), ints(dst), ints(&missing), ws.data_ptr(), need, int(src->size(0)),
+                                   int(c.L), int(c.S), int(c.Hkv), int(c.d), int(c.P), int(c.page), int(c.M),
+                                   stream_of(*c.refs));
+  if (status) return not_ok("fa_cache_fork", status);
   return THPVariable_Wrap(missing);
   END_HANDLE_TH_ERRORS
 }
@@ -290,8 +310,9 @@ PyObject* free_seqs(PyObject*, PyObject* const* a, Py_ssize_t n) {
   FA_IF(n == 5 && get_refs(a[0], c) && get_table(a[1], a[2], c) && get_int(a[4], page));
   const Tensor* seqs = dense_int(a[3], 1);
   FA_IF(seqs && fits({seqs->size(0)}));
-  FA_IF(fa_cache_free(ints(c.refs), ints(c.table), ints(c.lens), ints(seqs), int(seqs->size(0)), int(c.S),
-                      int(c.refs->size(0)), page, int(c.M), stream_of(*c.refs)) == FA_OK);
+  const int status = fa_cache_free(ints(c.refs), ints(c.table), ints(c.lens), ints(seqs), int(seqs->size(0)), int(c.S),
+                                   int(c.refs->size(0)), page, int(c.M), stream_of(*c.refs));
+  if (status) return not_ok("fa_cache_free", status);
   Py_RETURN_TRUE;
   END_HANDLE_TH_ERRORS
 }
@@ -305,9 +326,10 @@ PyObject* compact(PyObject*, PyObject* const* a, Py_ssize_t n) {
   const size_t need = fa_cache_workspace_size(int(c.S), int(c.P));
   FA_IF(need);
   const Tensor live = empty({1}, at::kInt, *c.refs), ws = bytes(need, *c.refs);
-  FA_IF(fa_cache_compact(c.k->data_ptr(), c.v->data_ptr(), ints(c.refs), ints(c.table), ints(c.lens), ints(&live),
-                         ws.data_ptr(), need, int(c.L), int(c.S), int(c.Hkv), int(c.d), int(c.P), int(c.page), int(c.M),
-                         stream_of(*c.refs)) == FA_OK);
+  const int status = fa_cache_compact(c.k->data_ptr(), c.v->data_ptr(), ints(c.refs), ints(c.table), ints(c.lens),
+                                      ints(&live), ws.data_ptr(), need, int(c.L), int(c.S), int(c.Hkv), int(c.d),
+                                      int(c.P), int(c.page), int(c.M), stream_of(*c.refs));
+  if (status) return not_ok("fa_cache_compact", status);
   return THPVariable_Wrap(live);
   END_HANDLE_TH_ERRORS
 }

@@ -1,0 +1,87 @@
+"""The compiled way through the window and cache bindings: what it does beside the call itself."""
+import os
+import subprocess
+import sys
+
+import pytest
+import torch
+
+ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module")
+def fa():
+    assert torch.cuda.is_available(), "GPU tests need a CUDA device"
+    from flashattention_bf16_fwd_b200 import cache, fa as binding, window
+    binding.cache, binding.window = cache, window
+    assert binding.fa_check_device_error() == 0
+    return binding
+
+
+def calls(fa):
+    """One small call of each entry point; the cache's leave it as it is."""
+    i32 = lambda x: torch.tensor(x, dtype=torch.int32, device="cuda")
+    rand = lambda *s: torch.randn(*s, device="cuda").bfloat16()
+    q, k, v, do = (rand(1, 2, 100, 64) for _ in range(4))
+    kp, vp, new = rand(1, 9, 2, 8, 64), rand(1, 9, 2, 8, 64), rand(2, 2, 64)
+    refs, table, lens = i32([1, 1] + [0] * 7), i32([[0, 1], [-1, -1]]), i32([10, 0])
+    zero, one = i32([0, 0]), i32([1])
+    o, lse = fa.window.attention_window_fwd(q, k, v, 20, 2)
+    return {
+        "window_fwd": lambda: fa.window.attention_window_fwd(q, k, v, 20, 2),
+        "window_bwd": lambda: fa.window.attention_window_bwd(q, k, v, o, lse, do, 20, 2),
+        "decode": lambda: fa.cache.attention_decode(new, kp[0], vp[0], table, lens),
+        "append": lambda: fa.cache.cache_append(new, new, kp[0], vp[0], table, lens),
+        "reserve": lambda: fa.cache.cache_reserve(refs, table, lens, zero, 8),
+        "fork": lambda: fa.cache.cache_fork(kp, vp, refs, table, lens, one, one),
+        "free": lambda: fa.cache.cache_free(refs, table, lens, one, 8),
+        "compact": lambda: fa.cache.cache_compact(kp, vp, refs, table, lens),
+    }
+
+
+FAILED_LAUNCH = """
+import ctypes, sys, torch
+from flashattention_bf16_fwd_b200 import cache, fa, window
+from tests.test_gpu_binding import calls
+fa.cache, fa.window = cache, window
+rt = ctypes.CDLL(next(line.split()[-1] for line in open("/proc/self/maps") if "libcudart.so" in line))
+tried = []
+class Lib:
+    def __getattr__(self, x):
+        tried.append(x)
+        return lambda *a: 0
+real = cache.lib
+for name, call in calls(fa).items():
+    stream = torch.cuda.Stream()
+    with torch.cuda.stream(stream):
+        for _ in range(2):                               # memory of this stream's own is at hand
+            call()
+        stream.synchronize()
+        tried.clear()
+        cache.lib = window.lib = Lib()
+        handle, graph = ctypes.c_void_p(stream.cuda_stream), ctypes.c_void_p()
+        assert rt.cudaStreamBeginCapture(handle, 2) == 0
+        assert rt.cudaStreamSynchronize(handle) != 0     # breaks the capture off: launches into it are refused
+        try:
+            call()
+            said = "nothing"
+        except fa.FAError as e:
+            said = e
+        cache.lib = window.lib = real
+        assert rt.cudaStreamEndCapture(handle, ctypes.byref(graph)) != 0
+        rt.cudaGetLastError()
+        print(name, "|", said, "|", tried)
+        call()
+        stream.synchronize()
+"""
+
+
+def test_a_failed_launch_is_said_and_not_tried_again(fa):
+    """A call whose launch failed may have run in part: a second one could pass over what the first has left.  (A
+    stream whose capture was broken off refuses launches; in a process of its own.)"""
+    r = subprocess.run([sys.executable, "-c", FAILED_LAUNCH], capture_output=True, text=True, timeout=300, cwd=ROOT)
+    assert r.returncode == 0, r.stderr
+    names = {"window_fwd": "fa_window_fwd", "window_bwd": "fa_window_bwd", "decode": "fa_decode", "append": "fa_cache_append",
+             "reserve": "fa_cache_reserve", "fork": "fa_cache_fork", "free": "fa_cache_free", "compact": "fa_cache_compact"}
+    assert r.stdout.splitlines() == [f"{name} | {fa.FAError(call, -7)} | []" for name, call in names.items()]
