@@ -7,7 +7,9 @@
 // None without having done anything where a call is not that, or where the
 // library refuses its arguments; window.py and cache.py then take their own way,
 // which says what is wrong.  A failed launch is raised here and not tried again:
-// part of the call may have run.  Host time of a call by that way and by this: windowed
+// part of the call may have run.  Other Python threads run while a call allocates
+// and launches, as they do while ctypes calls: a launch waits where the stream's
+// queue is full.  Host time of a call by that way and by this: windowed
 // forward 13.1 and 4.9 us, backward 22.4 and 10.9, decoding 18.5 and 7.6, append
 // 8.1 and 2.9, reserve 8.4 and 3.2, fork 15.6 and 6.3.
 #include <Python.h>
@@ -84,13 +86,13 @@ bool fits(std::initializer_list<int64_t> sizes) {
   return true;
 }
 
-Tensor empty(at::IntArrayRef sizes, at::ScalarType type, const Tensor& like) {
-  return at::detail::empty_cuda(sizes, type, like.device(), std::nullopt);
+Tensor empty(at::IntArrayRef sizes, at::ScalarType type, c10::Device on) {
+  return at::detail::empty_cuda(sizes, type, on, std::nullopt);
 }
 
-Tensor bytes(size_t n, const Tensor& like) { return empty({int64_t(n)}, at::kByte, like); }
+Tensor bytes(size_t n, c10::Device on) { return empty({int64_t(n)}, at::kByte, on); }
 
-void* stream_of(const Tensor& t) { return c10::cuda::getCurrentCUDAStream(t.get_device()).stream(); }
+void* stream_of(c10::Device on) { return c10::cuda::getCurrentCUDAStream(on.index()).stream(); }
 
 int32_t* ints(const Tensor* t) { return static_cast<int32_t*>(t->data_ptr()); }
 
@@ -114,6 +116,19 @@ PyObject* not_ok(const char* call, int status) {
   Py_XDECREF(fa);
   return r;
 }
+
+// Other Python threads run while one of these lives (an exception ends it too).
+// What the call needs of its tensors is read before.  0.1 us of a call's 2.1 to 9.
+class NoGil {
+ public:
+  NoGil() : state_(PyEval_SaveThread()) {}
+  ~NoGil() { PyEval_RestoreThread(state_); }
+  NoGil(const NoGil&) = delete;
+  NoGil& operator=(const NoGil&) = delete;
+
+ private:
+  PyThreadState* state_;
+};
 
 #define FA_IF(condition) \
   if (!(condition)) Py_RETURN_NONE
@@ -142,11 +157,20 @@ PyObject* window_fwd(PyObject*, PyObject* const* a, Py_ssize_t n) {
   float scale;
   FA_IF(n == 7 && get_heads(a, h) && get_int(a[3], window) && get_int(a[4], sinks) &&
         get_scale(a[5], h.q->size(3), scale) && get_int(a[6], fix_mode));
-  const auto s = h.q->sizes();
-  const Tensor o = empty(s, h.q->scalar_type(), *h.q), lse = empty(s.slice(0, 3), at::kFloat, *h.q);
-  const int status = fa_window_fwd(h.q->data_ptr(), h.k->data_ptr(), h.v->data_ptr(), o.data_ptr(),
-                                   lse.data_ptr<float>(), int(s[0]), int(s[1]), int(h.k->size(1)), int(s[2]),
-                                   int(s[3]), window, sinks, scale, fix_mode, h.elem, stream_of(*h.q));
+  const int B = int(h.q->size(0)), H = int(h.q->size(1)), Hkv = int(h.k->size(1)), N = int(h.q->size(2)),
+            d = int(h.q->size(3));
+  const at::ScalarType type = h.q->scalar_type();
+  const c10::Device on = h.q->device();
+  const void *q = h.q->data_ptr(), *k = h.k->data_ptr(), *v = h.v->data_ptr();
+  Tensor o, lse;
+  int status;
+  {
+    const NoGil no_gil;
+    o = empty({B, H, N, d}, type, on);
+    lse = empty({B, H, N}, at::kFloat, on);
+    status = fa_window_fwd(q, k, v, o.data_ptr(), lse.data_ptr<float>(), B, H, Hkv, N, d, window, sinks, scale,
+                           fix_mode, h.elem, stream_of(on));
+  }
   if (status) return not_ok("fa_window_fwd", status);
   return tuple_of(o, lse);
   END_HANDLE_TH_ERRORS
@@ -161,18 +185,27 @@ PyObject* window_bwd(PyObject*, PyObject* const* a, Py_ssize_t n) {
   FA_IF(n == 9 && get_heads(a, h) && get_int(a[6], window) && get_int(a[7], sinks) &&
         get_scale(a[8], h.q->size(3), scale));
   const auto s = h.q->sizes();
-  const Tensor *o = dense(a[3], h.q->scalar_type()), *lse = dense(a[4], at::kFloat),
-               *dout = dense(a[5], h.q->scalar_type());
-  FA_IF(o && lse && dout && o->sizes() == s && dout->sizes() == s && lse->sizes() == s.slice(0, 3));
+  const at::ScalarType type = h.q->scalar_type();
+  const Tensor *to = dense(a[3], type), *tlse = dense(a[4], at::kFloat), *tdout = dense(a[5], type);
+  FA_IF(to && tlse && tdout && to->sizes() == s && tdout->sizes() == s && tlse->sizes() == s.slice(0, 3));
   const int B = int(s[0]), H = int(s[1]), Hkv = int(h.k->size(1)), N = int(s[2]), d = int(s[3]);
   const size_t need = fa_window_bwd_workspace_size(B, H, Hkv, N, d, window, sinks);
   FA_IF(need);
-  const Tensor dq = empty(s, h.q->scalar_type(), *h.q), dk = empty(h.k->sizes(), h.q->scalar_type(), *h.q),
-               dv = empty(h.k->sizes(), h.q->scalar_type(), *h.q), ws = bytes(need, *h.q);
-  const int status = fa_window_bwd(h.q->data_ptr(), h.k->data_ptr(), h.v->data_ptr(), o->data_ptr(),
-                                   static_cast<const float*>(lse->data_ptr()), dout->data_ptr(), dq.data_ptr(),
-                                   dk.data_ptr(), dv.data_ptr(), ws.data_ptr(), need, B, H, Hkv, N, d, window, sinks,
-                                   scale, h.elem, stream_of(*h.q));
+  const c10::Device on = h.q->device();
+  const void *q = h.q->data_ptr(), *k = h.k->data_ptr(), *v = h.v->data_ptr(), *o = to->data_ptr(),
+             *dout = tdout->data_ptr();
+  const float* lse = static_cast<const float*>(tlse->data_ptr());
+  Tensor dq, dk, dv;
+  int status;
+  {
+    const NoGil no_gil;
+    dq = empty({B, H, N, d}, type, on);
+    dk = empty({B, Hkv, N, d}, type, on);
+    dv = empty({B, Hkv, N, d}, type, on);
+    const Tensor ws = bytes(need, on);
+    status = fa_window_bwd(q, k, v, o, lse, dout, dq.data_ptr(), dk.data_ptr(), dv.data_ptr(), ws.data_ptr(), need, B,
+                           H, Hkv, N, d, window, sinks, scale, h.elem, stream_of(on));
+  }
   if (status) return not_ok("fa_window_bwd", status);
   return tuple_of(dq, dk, dv);
   END_HANDLE_TH_ERRORS
@@ -180,9 +213,9 @@ PyObject* window_bwd(PyObject*, PyObject* const* a, Py_ssize_t n) {
 
 // The pages of one layer, or with `layers` of [L, ...] too, and the tables.
 struct Cache {
-  const Tensor *k, *v, *refs, *table, *lens;
-  int elem;
-  int64_t L, P, Hkv, page, d, S, M;
+  const Tensor *k = nullptr, *v = nullptr, *refs = nullptr, *table = nullptr, *lens = nullptr;
+  int elem = 0;
+  int64_t L = 0, P = 0, Hkv = 0, page = 0, d = 0, S = 0, M = 0;
 };
 
 bool get_pages(PyObject* k, PyObject* v, bool layers, Cache& c) {
@@ -217,6 +250,18 @@ int64_t row_stride(const Tensor* t, int64_t heads, int64_t d, at::ScalarType typ
   return t->stride(0);
 }
 
+// What the calls take of a cache, read before other threads may run.
+struct Raw {
+  void *k, *v;
+  int32_t *refs, *table, *lens;
+  int L, P, Hkv, page, d, S, M;
+  c10::Device on;
+  explicit Raw(const Cache& c)
+      : k(c.k ? c.k->data_ptr() : nullptr), v(c.v ? c.v->data_ptr() : nullptr), refs(c.refs ? ints(c.refs) : nullptr),
+        table(ints(c.table)), lens(ints(c.lens)), L(int(c.L)), P(int(c.P)), Hkv(int(c.Hkv)), page(int(c.page)),
+        d(int(c.d)), S(int(c.S)), M(int(c.M)), on(c.table->device()) {}
+};
+
 // (q, k_pages, v_pages, table, lens, window, sinks, scale) -> (o, lse)
 PyObject* decode(PyObject*, PyObject* const* a, Py_ssize_t n) {
   HANDLE_TH_ERRORS
@@ -225,17 +270,27 @@ PyObject* decode(PyObject*, PyObject* const* a, Py_ssize_t n) {
   float scale;
   FA_IF(n == 8 && get_pages(a[1], a[2], false, c) && get_table(a[3], a[4], c) &&
         (a[5] == Py_None || get_int(a[5], window)) && get_int(a[6], sinks) && get_scale(a[7], c.d, scale));
-  const Tensor* q = cuda_tensor(a[0]);
-  FA_IF(q && q->dim() == 3 && q->size(0) == c.S && q->size(1) > 0 && q->size(1) % c.Hkv == 0 && fits({q->size(1)}));
-  const int64_t stride = row_stride(q, q->size(1), c.d, c.k->scalar_type());
+  const Tensor* tq = cuda_tensor(a[0]);
+  FA_IF(tq && tq->dim() == 3 && tq->size(0) == c.S && tq->size(1) > 0 && tq->size(1) % c.Hkv == 0 &&
+        fits({tq->size(1)}));
+  const at::ScalarType type = c.k->scalar_type();
+  const int64_t stride = row_stride(tq, tq->size(1), c.d, type);
   FA_IF(stride > 0);
-  const int S = int(c.S), H = int(q->size(1)), Hkv = int(c.Hkv), d = int(c.d);
-  const size_t need = fa_decode_workspace_size(S, H, Hkv, d);
+  const Raw r(c);
+  const int H = int(tq->size(1));
+  const size_t need = fa_decode_workspace_size(r.S, H, r.Hkv, r.d);
   FA_IF(need);
-  const Tensor o = empty({S, H, d}, q->scalar_type(), *q), lse = empty({S, H}, at::kFloat, *q), ws = bytes(need, *q);
-  const int status = fa_decode(q->data_ptr(), c.k->data_ptr(), c.v->data_ptr(), ints(c.table), ints(c.lens),
-                               o.data_ptr(), lse.data_ptr<float>(), ws.data_ptr(), need, S, H, Hkv, d, int(c.P),
-                               int(c.page), int(c.M), stride, window, sinks, scale, c.elem, stream_of(*q));
+  const void* q = tq->data_ptr();
+  Tensor o, lse;
+  int status;
+  {
+    const NoGil no_gil;
+    o = empty({r.S, H, r.d}, type, r.on);
+    lse = empty({r.S, H}, at::kFloat, r.on);
+    const Tensor ws = bytes(need, r.on);
+    status = fa_decode(q, r.k, r.v, r.table, r.lens, o.data_ptr(), lse.data_ptr<float>(), ws.data_ptr(), need, r.S, H,
+                       r.Hkv, r.d, r.P, r.page, r.M, stride, window, sinks, scale, c.elem, stream_of(r.on));
+  }
   if (status) return not_ok("fa_decode", status);
   return tuple_of(o, lse);
   END_HANDLE_TH_ERRORS
@@ -246,16 +301,25 @@ PyObject* append(PyObject*, PyObject* const* a, Py_ssize_t n) {
   HANDLE_TH_ERRORS
   Cache c;
   FA_IF(n == 7 && get_pages(a[2], a[3], false, c) && get_table(a[4], a[5], c));
-  const Tensor *k = cuda_tensor(a[0]), *v = cuda_tensor(a[1]), *cu = nullptr;
-  const int64_t ks = row_stride(k, c.Hkv, c.d, c.k->scalar_type()), vs = row_stride(v, c.Hkv, c.d, c.k->scalar_type());
-  FA_IF(ks > 0 && vs > 0 && k->size(0) == v->size(0) && k->size(0) > 0 && fits({k->size(0)}));
+  const Tensor *tk = cuda_tensor(a[0]), *tv = cuda_tensor(a[1]);
+  const at::ScalarType type = c.k->scalar_type();
+  const int64_t ks = row_stride(tk, c.Hkv, c.d, type), vs = row_stride(tv, c.Hkv, c.d, type);
+  FA_IF(ks > 0 && vs > 0 && tk->size(0) == tv->size(0) && tk->size(0) > 0 && fits({tk->size(0)}));
+  const int32_t* cu = nullptr;
   if (a[6] != Py_None) {
-    cu = dense_int(a[6], 1);
-    FA_IF(cu && cu->size(0) == c.S + 1);
+    const Tensor* t = dense_int(a[6], 1);
+    FA_IF(t && t->size(0) == c.S + 1);
+    cu = ints(t);
   }
-  const int status = fa_cache_append(k->data_ptr(), v->data_ptr(), c.k->data_ptr(), c.v->data_ptr(), ints(c.table),
-                                     ints(c.lens), cu ? ints(cu) : nullptr, int(k->size(0)), int(c.S), int(c.Hkv),
-                                     int(c.d), int(c.P), int(c.page), int(c.M), ks, vs, stream_of(*c.k));
+  const Raw r(c);
+  const int T = int(tk->size(0));
+  const void *k = tk->data_ptr(), *v = tv->data_ptr();
+  int status;
+  {
+    const NoGil no_gil;
+    status = fa_cache_append(k, v, r.k, r.v, r.table, r.lens, cu, T, r.S, r.Hkv, r.d, r.P, r.page, r.M, ks, vs,
+                             stream_of(r.on));
+  }
   if (status) return not_ok("fa_cache_append", status);
   Py_RETURN_TRUE;
   END_HANDLE_TH_ERRORS
@@ -272,11 +336,18 @@ PyObject* reserve(PyObject*, PyObject* const* a, Py_ssize_t n) {
   Cache c;
   int page;
   FA_IF(n == 5 && get_refs(a[0], c) && get_table(a[1], a[2], c) && get_int(a[4], page));
-  const Tensor* add = dense_int(a[3], 1);
-  FA_IF(add && add->size(0) == c.S);
-  const Tensor missing = empty({1}, at::kInt, *c.refs);
-  const int status = fa_cache_reserve(ints(c.refs), ints(c.table), ints(c.lens), ints(add), ints(&missing), int(c.S),
-                                      int(c.refs->size(0)), page, int(c.M), stream_of(*c.refs));
+  const Tensor* tadd = dense_int(a[3], 1);
+  FA_IF(tadd && tadd->size(0) == c.S);
+  const Raw r(c);
+  const int P = int(c.refs->size(0));
+  const int32_t* add = ints(tadd);
+  Tensor missing;
+  int status;
+  {
+    const NoGil no_gil;
+    missing = empty({1}, at::kInt, r.on);
+    status = fa_cache_reserve(r.refs, r.table, r.lens, add, ints(&missing), r.S, P, page, r.M, stream_of(r.on));
+  }
   if (status) return not_ok("fa_cache_reserve", status);
   return THPVariable_Wrap(missing);
   END_HANDLE_TH_ERRORS
@@ -288,15 +359,22 @@ PyObject* fork(PyObject*, PyObject* const* a, Py_ssize_t n) {
   Cache c;
   FA_IF(n == 7 && get_pages(a[0], a[1], true, c) && get_refs(a[2], c) && get_table(a[3], a[4], c) &&
         c.refs->size(0) == c.P);
-  const Tensor *src = dense_int(a[5], 1), *dst = dense_int(a[6], 1);
-  FA_IF(src && dst && src->size(0) == dst->size(0) && fits({src->size(0)}));
-  const size_t need = fa_cache_workspace_size(int(c.S), int(c.P));
+  const Tensor *tsrc = dense_int(a[5], 1), *tdst = dense_int(a[6], 1);
+  FA_IF(tsrc && tdst && tsrc->size(0) == tdst->size(0) && fits({tsrc->size(0)}));
+  const Raw r(c);
+  const size_t need = fa_cache_workspace_size(r.S, r.P);
   FA_IF(need);
-  const Tensor missing = empty({1}, at::kInt, *c.refs), ws = bytes(need, *c.refs);
-  const int status = fa_cache_fork(c.k->data_ptr(), c.v->data_ptr(), ints(c.refs), ints(c.table), ints(c.lens),
-                                   ints(src), ints(dst), ints(&missing), ws.data_ptr(), need, int(src->size(0)),
-                                   int(c.L), int(c.S), int(c.Hkv), int(c.d), int(c.P), int(c.page), int(c.M),
-                                   stream_of(*c.refs));
+  const int F = int(tsrc->size(0));
+  const int32_t *src = ints(tsrc), *dst = ints(tdst);
+  Tensor missing;
+  int status;
+  {
+    const NoGil no_gil;
+    missing = empty({1}, at::kInt, r.on);
+    const Tensor ws = bytes(need, r.on);
+    status = fa_cache_fork(r.k, r.v, r.refs, r.table, r.lens, src, dst, ints(&missing), ws.data_ptr(), need, F, r.L,
+                           r.S, r.Hkv, r.d, r.P, r.page, r.M, stream_of(r.on));
+  }
   if (status) return not_ok("fa_cache_fork", status);
   return THPVariable_Wrap(missing);
   END_HANDLE_TH_ERRORS
@@ -308,10 +386,16 @@ PyObject* free_seqs(PyObject*, PyObject* const* a, Py_ssize_t n) {
   Cache c;
   int page;
   FA_IF(n == 5 && get_refs(a[0], c) && get_table(a[1], a[2], c) && get_int(a[4], page));
-  const Tensor* seqs = dense_int(a[3], 1);
-  FA_IF(seqs && fits({seqs->size(0)}));
-  const int status = fa_cache_free(ints(c.refs), ints(c.table), ints(c.lens), ints(seqs), int(seqs->size(0)), int(c.S),
-                                   int(c.refs->size(0)), page, int(c.M), stream_of(*c.refs));
+  const Tensor* tseqs = dense_int(a[3], 1);
+  FA_IF(tseqs && fits({tseqs->size(0)}));
+  const Raw r(c);
+  const int F = int(tseqs->size(0)), P = int(c.refs->size(0));
+  const int32_t* seqs = ints(tseqs);
+  int status;
+  {
+    const NoGil no_gil;
+    status = fa_cache_free(r.refs, r.table, r.lens, seqs, F, r.S, P, page, r.M, stream_of(r.on));
+  }
   if (status) return not_ok("fa_cache_free", status);
   Py_RETURN_TRUE;
   END_HANDLE_TH_ERRORS
@@ -323,12 +407,18 @@ PyObject* compact(PyObject*, PyObject* const* a, Py_ssize_t n) {
   Cache c;
   FA_IF(n == 5 && get_pages(a[0], a[1], true, c) && get_refs(a[2], c) && get_table(a[3], a[4], c) &&
         c.refs->size(0) == c.P);
-  const size_t need = fa_cache_workspace_size(int(c.S), int(c.P));
+  const Raw r(c);
+  const size_t need = fa_cache_workspace_size(r.S, r.P);
   FA_IF(need);
-  const Tensor live = empty({1}, at::kInt, *c.refs), ws = bytes(need, *c.refs);
-  const int status = fa_cache_compact(c.k->data_ptr(), c.v->data_ptr(), ints(c.refs), ints(c.table), ints(c.lens),
-                                      ints(&live), ws.data_ptr(), need, int(c.L), int(c.S), int(c.Hkv), int(c.d),
-                                      int(c.P), int(c.page), int(c.M), stream_of(*c.refs));
+  Tensor live;
+  int status;
+  {
+    const NoGil no_gil;
+    live = empty({1}, at::kInt, r.on);
+    const Tensor ws = bytes(need, r.on);
+    status = fa_cache_compact(r.k, r.v, r.refs, r.table, r.lens, ints(&live), ws.data_ptr(), need, r.L, r.S, r.Hkv, r.d,
+                              r.P, r.page, r.M, stream_of(r.on));
+  }
   if (status) return not_ok("fa_cache_compact", status);
   return THPVariable_Wrap(live);
   END_HANDLE_TH_ERRORS

@@ -2,6 +2,8 @@
 import os
 import subprocess
 import sys
+import threading
+import time
 
 import pytest
 import torch
@@ -38,6 +40,39 @@ def calls(fa):
         "free": lambda: fa.cache.cache_free(refs, table, lens, one, 8),
         "compact": lambda: fa.cache.cache_compact(kp, vp, refs, table, lens),
     }
+
+
+@pytest.mark.parametrize("name", ["window_fwd", "window_bwd", "decode", "append", "reserve", "fork", "free", "compact"])
+def test_other_threads_run_while_a_launch_waits(fa, name):
+    """A stream that is busy for half a second or more and its queue of launches full: the call waits for room, and
+    another Python thread goes on meanwhile."""
+    call = calls(fa)[name]
+    for _ in range(3):
+        call()
+    torch.cuda.synchronize()
+    gaps, stop = [], threading.Event()
+
+    def tick():
+        last = time.perf_counter()
+        while not stop.is_set():
+            time.sleep(0.001)
+            now = time.perf_counter()
+            gaps.append(now - last)
+            last = now
+    other = threading.Thread(target=tick)
+    torch.cuda._sleep(1_500_000_000)                    # cycles of a clock of at most 2 GHz
+    other.start()
+    longest = 0.0
+    for _ in range(2500):
+        begin = time.perf_counter()
+        call()
+        longest = max(longest, time.perf_counter() - begin)
+    stop.set()
+    other.join()
+    torch.cuda.synchronize()
+    assert fa.fa_check_device_error() == 0
+    assert longest > 0.3, "no launch waited"
+    assert max(gaps) < 0.2
 
 
 FAILED_LAUNCH = """
