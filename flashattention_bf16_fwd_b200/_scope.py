@@ -63,6 +63,9 @@ INT_MAX = 2**31 - 1
 
 
 def count(n) -> int:
-    """n as a C int: more than an int holds is as much as the largest one, less than nothing is -1."""
-    n = int(n)
-    return n if 0 <= n <= INT_MAX else INT_MAX if n > 0 else -1
+    """n, a whole number of any type, as a C int: more than an int holds is as much as the largest one, less than
+    nothing is -1."""
+    i = int(n)
+    if i != n:
+        raise ValueError(f"{n} is not a whole number")
+    return i if 0 <= i <= INT_MAX else INT_MAX if i > 0 else -1
