@@ -2,7 +2,9 @@
 the module _fast (csrc/fast.cpp) through which the window and cache bindings call it.
 
 Run ``python -m flashattention_bf16_fwd_b200.build`` (or ``__graft_entry__.build()``).
-nvcc cross-compiles for sm_100a; no GPU is needed to build.
+nvcc cross-compiles for sm_100a; no GPU is needed to build.  The library needs
+nothing else; where torch or Python's headers are missing the module is left out,
+with a line on stderr (importing the bindings then says what is missing).
 """
 from __future__ import annotations
 
@@ -53,16 +55,24 @@ def build(force: bool = False, verbose: bool = False, extra=()) -> str:
     return LIB
 
 
-def build_fast(force: bool = False, verbose: bool = False) -> str:
-    """The module _fast: C++ against this interpreter's and torch's headers."""
+def build_fast(force: bool = False, verbose: bool = False) -> str | None:
+    """The module _fast: C++ against this interpreter's and torch's headers (None: they are not there)."""
     headers = [os.path.join(ROOT, "include", f) for f in ("fa_b200.h", "fa_b200_cache.h", "fa_b200_window.h")]
     if not force and up_to_date(FAST, [FAST_SOURCE] + headers):
         return FAST
-    import torch
+    python = sysconfig.get_paths()["include"]
+    try:
+        import torch
+    except ImportError as e:
+        print(f"{FAST} is not built, torch is missing: {e}", file=sys.stderr)
+        return None
+    if not os.path.exists(os.path.join(python, "Python.h")):
+        print(f"{FAST} is not built, there is no Python.h in {python}", file=sys.stderr)
+        return None
     home = os.path.dirname(torch.__file__)
     cuda = os.environ.get("CUDA_HOME", "/usr/local/cuda")
     includes = [os.path.join(home, "include"), os.path.join(home, "include", "torch", "csrc", "api", "include"),
-                os.path.join(cuda, "include"), sysconfig.get_paths()["include"]]
+                os.path.join(cuda, "include"), python]
     cmd = ["g++", "-O2", "-std=c++17", "-shared", "-fPIC", "-fvisibility=hidden",
            f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}", *(f"-I{d}" for d in includes),
            "-o", FAST, FAST_SOURCE, "-L" + PKG, "-lfa_b200", "-Wl,-rpath,$ORIGIN",
