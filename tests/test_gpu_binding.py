@@ -75,6 +75,59 @@ def test_other_threads_run_while_a_launch_waits(fa, name):
     assert max(gaps) < 0.2
 
 
+def test_two_threads_at_once(fa):
+    """Steps of two Python threads, each with its own stream and tensors, are those of one after the other."""
+    from test_gpu_window_dq import draw, same, spread
+    jobs = []
+    for seed, (H, Hkv, N, d, dt, window) in enumerate([(8, 4, 900, 64, "bf16", 200), (6, 2, 700, 128, "fp16", 333)]):
+        x = draw(1, H, Hkv, N, d, dt, seed)
+        g = torch.Generator(device="cuda").manual_seed(seed)
+        rand = lambda *s: torch.randn(*s, generator=g, device="cuda").to(x[0].dtype)
+        q, k, v = rand(9, H, d), rand(9, Hkv, d), rand(9, Hkv, d)
+
+        def job(x=x, q=q, k=k, v=v, window=window, Hkv=Hkv, d=d):
+            """A training step, and a cache from its first token on."""
+            o, lse = fa.window.attention_window_fwd(*x[:3], window, 4)
+            out = [o, lse, *fa.window.attention_window_bwd(*x[:3], o, lse, x[3], window, 4)]
+            kp, vp = (torch.zeros(2, 60, Hkv, 8, d, dtype=q.dtype, device="cuda") for _ in range(2))
+            refs, lens = (torch.zeros(n, dtype=torch.int32, device="cuda") for n in (60, 9))
+            table = torch.full((9, 6), -1, dtype=torch.int32, device="cuda")
+            one = torch.ones(9, dtype=torch.int32, device="cuda")
+            one[6:] = 0
+            src, dst = torch.arange(3, device="cuda").int(), torch.arange(6, 9, device="cuda").int()
+            for _ in range(11):
+                out.append(fa.cache.cache_reserve(refs, table, lens, one, 8))
+                fa.cache.cache_append(k, v, kp[1], vp[1], table, lens)
+                out += fa.cache.attention_decode(q, kp[1], vp[1], table, lens, window=5, sinks=1)
+            out.append(fa.cache.cache_fork(kp, vp, refs, table, lens, src, dst))
+            fa.cache.cache_free(refs, table, lens, src, 8)
+            out.append(fa.cache.cache_compact(kp, vp, refs, table, lens))
+            return out + [kp, vp, refs, table, lens]
+        jobs.append((job, spread(x, window, 4)))
+    want = [job() for job, _ in jobs]
+    torch.cuda.synchronize()
+    got, failed, start = [None, None], [], threading.Barrier(2)
+
+    def run(i):
+        try:
+            with torch.cuda.stream(torch.cuda.Stream()):
+                start.wait(60)
+                got[i] = [jobs[i][0]() for _ in range(8)]
+        except Exception as e:                          # reported by the test's own thread
+            failed.append(e)
+    threads = [threading.Thread(target=run, args=(i,)) for i in range(2)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    torch.cuda.synchronize()
+    assert not failed and fa.fa_check_device_error() == 0
+    for runs, w, (_, noise) in zip(got, want, jobs):
+        for one in runs:
+            same(one[2], w[2], noise)
+            assert all(torch.equal(a, b) for i, (a, b) in enumerate(zip(one, w)) if i != 2)
+
+
 FAILED_LAUNCH = """
 import ctypes, sys, torch
 from flashattention_bf16_fwd_b200 import cache, fa, window
