@@ -18,7 +18,9 @@ A decoding step::
 
 Nothing synchronises: lengths, pages and outcomes stay on the device (a call
 that found one out of range is reported by ``fa.fa_check_device_error``), and a
-step can be captured into a CUDA graph.
+step can be captured into a CUDA graph.  Calls on one cache are put in order by
+the caller: by one stream, and among Python threads by a lock (a call lets other
+threads run while it launches).
 """
 from __future__ import annotations
 

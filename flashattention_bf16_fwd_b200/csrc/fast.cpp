@@ -1,7 +1,7 @@
 // fast.cpp - the short way through the window and cache bindings (module _fast).
 //
 // For a short sequence the kernels take a few microseconds, and the Python
-// binding's checks, allocations and ctypes call take 8 to 20.  Each function here
+// binding's checks, allocations and ctypes call take 6 to 20.  Each function here
 // does the same in one step for the common call: tensors of the right shapes on
 // the current device, the current stream, a workspace of its own.  It returns
 // None without having done anything where a call is not that, or where the
@@ -9,9 +9,10 @@
 // which says what is wrong.  A failed launch is raised here and not tried again:
 // part of the call may have run.  Other Python threads run while a call allocates
 // and launches, as they do while ctypes calls: a launch waits where the stream's
-// queue is full.  Host time of a call by that way and by this: windowed
-// forward 13.1 and 4.9 us, backward 22.4 and 10.9, decoding 18.5 and 7.6, append
-// 8.1 and 2.9, reserve 8.4 and 3.2, fork 15.6 and 6.3.
+// queue is full.  Host time of a call by ctypes and by this way: windowed forward
+// 12.4 and 4.8 us, backward 19.8 and 9.1, decoding 15.7 and 5.1, append 8.1 and
+// 2.8, reserve 8.6 and 3.3, fork 15.6 and 6.1, free 6.4 and 2.3, compact 14.3 and
+// 6.4.
 #include <Python.h>
 
 #include <ATen/core/Tensor.h>
