@@ -72,7 +72,7 @@ def test_other_threads_run_while_a_launch_waits(fa, name):
     torch.cuda.synchronize()
     assert fa.fa_check_device_error() == 0
     assert longest > 0.3, "no launch waited"
-    assert max(gaps) < 0.2
+    assert max(gaps) < longest / 2                      # a call that keeps the others out makes a gap as long as it waits
 
 
 def test_two_threads_at_once(fa):
